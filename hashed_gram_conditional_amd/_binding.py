@@ -27,6 +27,12 @@ GATE_SIGNED_SQRT = 0
 GATE_PLAIN = 1
 MAX_CONV_TAPS = 8
 MAX_CONV_HISTORY = 64
+BF16 = 0
+F32 = 1
+MX_E4M3 = 0
+MX_E2M1 = 1
+MAX_EMBED_DIM = 32768
+MAX_EMBED_GRAD_IDS = 1 << 28
 
 OK, EINVAL, EVOCAB, EMULT, ESHAPE, EWORKSPACE, EHIP, EPRIMES, ESCRATCH = \
     0, -1, -2, -3, -4, -5, -6, -7, -8
@@ -87,6 +93,19 @@ class ShortConv(ctypes.Structure):
     ]
 
 
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [
+        ("table_rows", ctypes.c_int64),
+        ("n_ids", ctypes.c_int64),
+        ("table_ld", ctypes.c_int64),
+        ("out_ld", ctypes.c_int64),
+        ("dim", ctypes.c_int32),
+        ("table_type", ctypes.c_int32),
+        ("out_type", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is not built; run __graft_entry__.build() "
@@ -140,6 +159,14 @@ def _load():
         "engram_forward_static": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P, P, P]),
         "engram_forward_static_max_bytes": (SZ, []),
         "engram_transpose": (ctypes.c_int, [P, P, I64, I64, I64, I32, P]),
+        "engram_sizeof_embed_desc": (SZ, []),
+        "engram_embed": (ctypes.c_int, [P, P, P, P, P]),
+        "engram_embed_grad_workspace_size": (SZ, [P]),
+        "engram_embed_grad": (ctypes.c_int, [P, P, P, P, P, P, P, SZ, P]),
+        "engram_embed_grad_dense": (ctypes.c_int, [P, P, P, P, I32, P, SZ, P]),
+        "engram_quantize_mx4": (ctypes.c_int, [P, I32, I64, I64, I64, I64, P, P, P, P]),
+        "engram_project_mx4": (ctypes.c_int, [P, P, I32, P, P, P, I64, I64, I64, P, SZ, P]),
+        "engram_project_mx4_workspace_size": (SZ, [I64, I64, I64, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -151,6 +178,8 @@ def _load():
         raise ImportError("engram_forward_desc layout mismatch between binding and library")
     if lib.engram_sizeof_short_conv() != ctypes.sizeof(ShortConv):
         raise ImportError("engram_short_conv layout mismatch between binding and library")
+    if lib.engram_sizeof_embed_desc() != ctypes.sizeof(EmbedDesc):
+        raise ImportError("engram_embed_desc layout mismatch between binding and library")
     return lib
 
 
@@ -234,6 +263,15 @@ def short_conv(weight, taps: int = 4, dilation: int = 3, eps: float = 1e-6, norm
     c.state_v_in, c.state_s_in = _ptr(state_v_in), _ptr(state_s_in)
     c.state_v_out, c.state_s_out = _ptr(state_v_out), _ptr(state_s_out)
     return c
+
+
+def embed_desc(table_rows: int, n_ids: int, dim: int, table_type: int = BF16,
+               out_type: int = BF16, scale: float = 1.0, table_ld: int = 0,
+               out_ld: int = 0) -> EmbedDesc:
+    d = EmbedDesc()
+    d.table_rows, d.n_ids, d.table_ld, d.out_ld = table_rows, n_ids, table_ld, out_ld
+    d.dim, d.table_type, d.out_type, d.scale = dim, table_type, out_type, scale
+    return d
 
 
 def engram_make_primes(base: int, count: int):
@@ -443,3 +481,52 @@ def engram_forward_conv(params: HashParams, desc: ForwardDesc, conv: ShortConv, 
                                    _ptr(wkv), _ptr(q_w), _ptr(k_w), _ptr(h), _ptr(gate_out),
                                    _ptr(workspace), workspace_bytes, _stream(stream)),
            "engram_forward_conv")
+
+
+def engram_embed(desc: EmbedDesc, table, row_ids, out, stream=None):
+    """out[i] = scale * table[row_ids[i]]; zero rows for ids outside the table."""
+    _check(LIB.engram_embed(ctypes.byref(desc), _table_ptr(table), _ptr(row_ids), _ptr(out),
+                            _stream(stream)), "engram_embed")
+
+
+def engram_embed_grad_workspace_size(desc: EmbedDesc) -> int:
+    return int(LIB.engram_embed_grad_workspace_size(ctypes.byref(desc)))
+
+
+def engram_embed_grad(desc: EmbedDesc, d_out, row_ids, grad_rows, grad, n_rows, workspace,
+                      workspace_bytes: int, stream=None):
+    """The touched rows in ascending order (then -1), their fp32 gradients and their number."""
+    _check(LIB.engram_embed_grad(ctypes.byref(desc), _ptr(d_out), _ptr(row_ids), _ptr(grad_rows),
+                                 _ptr(grad), _ptr(n_rows), _ptr(workspace), workspace_bytes,
+                                 _stream(stream)), "engram_embed_grad")
+
+
+def engram_embed_grad_dense(desc: EmbedDesc, d_out, row_ids, grad, accumulate: int, workspace,
+                            workspace_bytes: int, stream=None):
+    """The fp32 gradient of the whole table, overwritten (0) or added to (1)."""
+    _check(LIB.engram_embed_grad_dense(ctypes.byref(desc), _ptr(d_out), _ptr(row_ids), _ptr(grad),
+                                       accumulate, _ptr(workspace), workspace_bytes,
+                                       _stream(stream)), "engram_embed_grad_dense")
+
+
+def engram_quantize_mx4(src, src_type: int, rows: int, cols: int, src_ld: int, out_cols: int,
+                        codes, scales, values=None, stream=None):
+    """E2M1 codes and E8M0 block scales of src (and the values they stand for)."""
+    _check(LIB.engram_quantize_mx4(_ptr(src), src_type, rows, cols, src_ld, out_cols, _ptr(codes),
+                                   _ptr(scales), _ptr(values), _stream(stream)),
+           "engram_quantize_mx4")
+
+
+def engram_project_mx4_workspace_size(tokens: int, in_dim: int, out_dim: int,
+                                      e_format: int) -> int:
+    return int(LIB.engram_project_mx4_workspace_size(tokens, in_dim, out_dim, e_format))
+
+
+def engram_project_mx4(e_codes, e_scales, e_format: int, w_codes, w_scales, kv, tokens: int,
+                       in_dim: int, out_dim: int, workspace=None, workspace_bytes: int = 0,
+                       stream=None):
+    """The projection with a 4-bit weight (e in 8 or 4 bits)."""
+    _check(LIB.engram_project_mx4(_ptr(e_codes), _ptr(e_scales), e_format, _ptr(w_codes),
+                                  _ptr(w_scales), _ptr(kv), tokens, in_dim, out_dim,
+                                  _ptr(workspace), workspace_bytes, _stream(stream)),
+           "engram_project_mx4")

@@ -170,4 +170,14 @@ struct EngramConvArgs {
   float *state_s_out;
 };
 
+// The scaled lookup and its gradient (embed.hip, embed_grad.hip); strides resolved.
+struct EngramEmbedArgs {
+  int64_t table_rows, n_ids;
+  int64_t table_ld, out_ld;
+  int64_t grad_ld;               // rows of the gradient (embed_grad.hip only)
+  int dim;
+  int table_f32, out_f32;
+  float scale;
+};
+
 #include "launchers.h"

@@ -1,6 +1,7 @@
 // C ABI of the Engram layer forward: argument validation on the host, then the
 // stage launches on the caller's stream. Declarations and the contract of every
 // entry point are in include/engram.h.
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -283,6 +284,51 @@ int resolve_table(const void *table, int64_t table_rows, const void **dev, bool 
   return ENGRAM_EINVAL;
 }
 
+bool float_type_ok(int32_t t) { return t == ENGRAM_BF16 || t == ENGRAM_F32; }
+
+// A row stride of the lookup: 0 means dim.
+int embed_stride(int64_t ld, int32_t dim, int64_t *out) {
+  if (ld == 0) ld = dim;
+  if (ld < dim || ld > INT32_MAX) return ENGRAM_ESHAPE;
+  *out = ld;
+  return ENGRAM_OK;
+}
+
+// The largest n_ids * dim: keeps (values of the output) * dim below 2^64, the
+// bound of the kernels' division.
+constexpr int64_t kMaxEmbedValues = (int64_t)1 << 48;
+
+int make_embed_args(const engram_embed_desc *d, EngramEmbedArgs *a) {
+  if (d == nullptr) return ENGRAM_EINVAL;
+  if (d->table_rows < 0 || d->n_ids < 0) return ENGRAM_ESHAPE;
+  if (d->dim < 1 || d->dim > ENGRAM_MAX_EMBED_DIM) return ENGRAM_ESHAPE;
+  if (d->n_ids > kMaxEmbedValues / d->dim) return ENGRAM_ESHAPE;
+  if (!float_type_ok(d->table_type) || !float_type_ok(d->out_type)) return ENGRAM_EINVAL;
+  if (!isfinite(d->scale)) return ENGRAM_EINVAL;
+  int rc = embed_stride(d->table_ld, d->dim, &a->table_ld);
+  if (rc == ENGRAM_OK) rc = embed_stride(d->out_ld, d->dim, &a->out_ld);
+  if (rc != ENGRAM_OK) return rc;
+  a->table_rows = d->table_rows;
+  a->n_ids = d->n_ids;
+  a->grad_ld = d->dim;
+  a->dim = d->dim;
+  a->table_f32 = d->table_type == ENGRAM_F32;
+  a->out_f32 = d->out_type == ENGRAM_F32;
+  a->scale = d->scale;
+  return ENGRAM_OK;
+}
+
+// The gradient sorts 32-bit keys, table_rows itself among them, and numbers the
+// ids in 32 bits.
+int make_embed_grad_args(const engram_embed_desc *d, bool dense, EngramEmbedArgs *a) {
+  const int rc = make_embed_args(d, a);
+  if (rc != ENGRAM_OK) return rc;
+  if (d->table_rows > (int64_t)UINT32_MAX - 1 || d->n_ids > ENGRAM_MAX_EMBED_GRAD_IDS)
+    return ENGRAM_ESHAPE;
+  if (dense) a->grad_ld = a->table_ld;
+  return ENGRAM_OK;
+}
+
 // The last HIP error an entry point returned ENGRAM_EHIP for, per host thread.
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
@@ -319,6 +365,8 @@ size_t engram_sizeof_hash_params(void) { return sizeof(engram_hash_params); }
 size_t engram_sizeof_forward_desc(void) { return sizeof(engram_forward_desc); }
 
 size_t engram_sizeof_short_conv(void) { return sizeof(engram_short_conv); }
+
+size_t engram_sizeof_embed_desc(void) { return sizeof(engram_embed_desc); }
 
 int engram_make_primes(int64_t base, int32_t count, int64_t *primes_out, int64_t *offsets_out,
                        int64_t *total_rows_out) {
@@ -1098,6 +1146,121 @@ int engram_forward_static(const engram_hash_params *params, const engram_forward
   return forward_impl(params, desc, nullptr, ids, hist_in, hist_out, table, wkv, q_w, k_w, h,
                       gate_out, ws, ENGRAM_STATIC_SCRATCH_BYTES, stream,
                       /*gemm_ws_optional=*/true);
+}
+
+int engram_embed(const engram_embed_desc *desc, const void *table, const int64_t *row_ids,
+                 void *out, hipStream_t stream) {
+  EngramEmbedArgs a;
+  int rc = make_embed_args(desc, &a);
+  if (rc != ENGRAM_OK) return rc;
+  if (a.n_ids == 0) return ENGRAM_OK;
+  if (row_ids == nullptr || out == nullptr || (table == nullptr && a.table_rows > 0))
+    return ENGRAM_EINVAL;
+  if (!aligned(table, 16) || !aligned(row_ids, 8) || !aligned(out, 16)) return ENGRAM_EINVAL;
+  bool host = false;
+  rc = resolve_table(table, a.table_rows, &table, &host);
+  if (rc != ENGRAM_OK) return rc;
+  return hip_status(engram_launch_embed(a, table, row_ids, out, host, stream));
+}
+
+size_t engram_embed_grad_workspace_size(const engram_embed_desc *desc) {
+  EngramEmbedArgs a;
+  if (make_embed_grad_args(desc, false, &a) != ENGRAM_OK) return 0;
+  return engram_embed_grad_workspace(a);
+}
+
+int engram_embed_grad(const engram_embed_desc *desc, const void *d_out, const int64_t *row_ids,
+                      int64_t *grad_rows, float *grad, int64_t *n_rows, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream) {
+  EngramEmbedArgs a;
+  const int rc = make_embed_grad_args(desc, false, &a);
+  if (rc != ENGRAM_OK) return rc;
+  if (n_rows == nullptr || !aligned(n_rows, 8)) return ENGRAM_EINVAL;
+  if (a.n_ids > 0 && (d_out == nullptr || row_ids == nullptr || grad_rows == nullptr ||
+                      grad == nullptr))
+    return ENGRAM_EINVAL;
+  if (!aligned(d_out, 16) || !aligned(row_ids, 8) || !aligned(grad_rows, 8) || !aligned(grad, 16))
+    return ENGRAM_EINVAL;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < engram_embed_grad_workspace(a))
+    return ENGRAM_EWORKSPACE;
+  return hip_status(engram_launch_embed_grad(a, d_out, row_ids, grad, grad_rows, n_rows, 0,
+                                             workspace, stream));
+}
+
+int engram_embed_grad_dense(const engram_embed_desc *desc, const void *d_out,
+                            const int64_t *row_ids, float *grad, int32_t accumulate,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  EngramEmbedArgs a;
+  const int rc = make_embed_grad_args(desc, true, &a);
+  if (rc != ENGRAM_OK) return rc;
+  if (accumulate != 0 && accumulate != 1) return ENGRAM_EINVAL;
+  if (a.table_rows == 0 || (a.n_ids == 0 && accumulate)) return ENGRAM_OK;
+  if (grad == nullptr || (a.n_ids > 0 && (d_out == nullptr || row_ids == nullptr)))
+    return ENGRAM_EINVAL;
+  if (!aligned(d_out, 16) || !aligned(row_ids, 8) || !aligned(grad, 16)) return ENGRAM_EINVAL;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < engram_embed_grad_workspace(a))
+    return ENGRAM_EWORKSPACE;
+  return hip_status(engram_launch_embed_grad(a, d_out, row_ids, grad, nullptr, nullptr, accumulate,
+                                             workspace, stream));
+}
+
+int engram_quantize_mx4(const void *src, int32_t src_type, int64_t rows, int64_t cols,
+                        int64_t src_ld, int64_t out_cols, void *codes, void *scales,
+                        void *values, hipStream_t stream) {
+  if (!float_type_ok(src_type)) return ENGRAM_EINVAL;
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || out_cols < cols || out_cols % 32 != 0 ||
+      out_cols > ((int64_t)1 << 20))
+    return ENGRAM_ESHAPE;
+  if (rows > ((int64_t)1 << 40) / out_cols) return ENGRAM_ESHAPE;
+  if (src_ld == 0) src_ld = cols;
+  if (src_ld < cols || src_ld > INT32_MAX) return ENGRAM_ESHAPE;
+  if (rows == 0) return ENGRAM_OK;
+  if (src == nullptr || codes == nullptr || scales == nullptr) return ENGRAM_EINVAL;
+  if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(values, 16))
+    return ENGRAM_EINVAL;
+  return hip_status(engram_launch_quantize_mx4(src_type == ENGRAM_F32, src, rows, cols, src_ld,
+                                               out_cols, (uint8_t *)codes, (uint8_t *)scales,
+                                               values, stream));
+}
+
+size_t engram_project_mx4_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim,
+                                         int32_t e_format) {
+  if (tokens <= 0 || in_dim < 128 || in_dim % 128 != 0 || out_dim < 1) return 0;
+  if (e_format != ENGRAM_MX_E4M3 && e_format != ENGRAM_MX_E2M1) return 0;
+  size_t bytes = 0;
+  if (engram_gemm_mx4_workspace(tokens, out_dim, in_dim, e_format == ENGRAM_MX_E2M1, &bytes) !=
+      hipSuccess)
+    return 0;
+  return bytes;
+}
+
+int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_format,
+                       const void *w_codes, const void *w_scales, void *kv, int64_t tokens,
+                       int64_t in_dim, int64_t out_dim, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream) {
+  if (e_format != ENGRAM_MX_E4M3 && e_format != ENGRAM_MX_E2M1) return ENGRAM_EINVAL;
+  if (tokens < 0 || tokens > INT32_MAX || in_dim < 128 || in_dim % 128 != 0 || out_dim < 1 ||
+      out_dim % 8 != 0 || out_dim > INT32_MAX)
+    return ENGRAM_ESHAPE;
+  if (!bf16_projection_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
+  if (tokens == 0) return ENGRAM_OK;
+  if (e_codes == nullptr || e_scales == nullptr || w_codes == nullptr || w_scales == nullptr ||
+      kv == nullptr)
+    return ENGRAM_EINVAL;
+  if (!aligned(e_codes, 16) || !aligned(e_scales, 4) || !aligned(w_codes, 16) ||
+      !aligned(w_scales, 4) || !aligned(kv, 16))
+    return ENGRAM_EINVAL;
+  if (workspace != nullptr) {
+    if (!aligned(workspace, 256) ||
+        workspace_bytes < engram_project_mx4_workspace_size(tokens, in_dim, out_dim, e_format))
+      return ENGRAM_EWORKSPACE;
+  }
+  return hip_status(engram_launch_gemm_mx4((const uint8_t *)w_codes, (const uint8_t *)w_scales,
+                                           (const uint8_t *)e_codes, (const uint8_t *)e_scales,
+                                           e_format == ENGRAM_MX_E2M1, (uint16_t *)kv, tokens,
+                                           out_dim, in_dim, workspace, workspace_bytes, stream));
 }
 
 }  // extern "C"

@@ -120,3 +120,29 @@ hipError_t engram_launch_short_conv(bool f32, const EngramConvArgs &c, const int
 // 4-byte elements (layout.hip).
 hipError_t engram_launch_transpose(const void *src, void *dst, int64_t rows, int64_t cols,
                                    int64_t dst_ld, int elem_bytes, hipStream_t stream);
+
+hipError_t engram_launch_embed(const EngramEmbedArgs &a, const void *table,
+                               const int64_t *row_ids, void *out, bool host_table,
+                               hipStream_t stream);
+
+// The table's gradient by sorted ids. n_rows set: the touched rows side by side;
+// NULL: into the dense array grad, overwritten or (accumulate) added to. The workspace holds engram_embed_grad_workspace bytes.
+size_t engram_embed_grad_workspace(const EngramEmbedArgs &a);
+hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
+                                    const int64_t *row_ids, float *grad, int64_t *grad_rows,
+                                    int64_t *n_rows, int accumulate, void *workspace,
+                                    hipStream_t stream);
+
+// E2M1 codes [rows, out_cols / 2] and E8M0 scales [rows, out_cols / 32] of a [rows,
+// cols] array; values (or NULL) as src.
+hipError_t engram_launch_quantize_mx4(bool f32, const void *src, int64_t rows, int64_t cols,
+                                      int64_t ld, int64_t out_cols, uint8_t *codes,
+                                      uint8_t *scales, void *values, hipStream_t stream);
+
+// Projection with a 4-bit weight: W codes [n, k / 2], e codes [m, k / 2] (e_fp4) or
+// E4M3 [m, k], scales [.., k / 32]; kv bf16 [m, n].
+hipError_t engram_launch_gemm_mx4(const uint8_t *w_codes, const uint8_t *w_scales,
+                                  const uint8_t *e_codes, const uint8_t *e_scales, bool e_fp4,
+                                  uint16_t *kv, int64_t m, int64_t n, int64_t k, void *workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+hipError_t engram_gemm_mx4_workspace(int64_t m, int64_t n, int64_t k, bool e_fp4, size_t *bytes);

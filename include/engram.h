@@ -51,7 +51,8 @@
  * prefetch on a separate path, wait for its completion event, stall =
  * max(0, T_fetch - T_window); [P3] §五: the host link's bandwidth is the cost).
  * Every entry point that reads a table (engram_gather, engram_gather_rows,
- * engram_gather_mx, engram_forward, engram_forward_conv, engram_forward_mx)
+ * engram_gather_mx, engram_embed, engram_forward, engram_forward_conv,
+ * engram_forward_mx)
  * accepts pinned host memory (hipHostMalloc, or torch's pin_memory) as well as
  * device memory: its kernels then read the 264-byte rows over the host link
  * themselves, straight into HBM, with no staging copy on the host. A prefetch is
@@ -182,6 +183,37 @@ typedef struct engram_short_conv {
   float *state_s_out;         /*   (both NULL or both set); may equal the inputs   */
 } engram_short_conv;
 
+/* Element types of engram_embed, its gradient and engram_quantize_mx4. */
+typedef enum engram_float_type {
+  ENGRAM_BF16 = 0,
+  ENGRAM_F32 = 1
+} engram_float_type;
+
+/* Element formats of engram_project_mx4's e operand; both carry one E8M0 scale
+ * (2^(s - 127), 0xFF = NaN) per 32 consecutive inputs. */
+typedef enum engram_mx_format {
+  ENGRAM_MX_E4M3 = 0,         /* one byte per value (engram_gather_mx)             */
+  ENGRAM_MX_E2M1 = 1          /* two values per byte, the lower column in the low
+                                 half (engram_quantize_mx4)                        */
+} engram_mx_format;
+
+#define ENGRAM_MAX_EMBED_DIM 32768
+#define ENGRAM_MAX_EMBED_GRAD_IDS (1ll << 28)
+
+/* Shapes and types of engram_embed and of its gradient. */
+typedef struct engram_embed_desc {
+  int64_t table_rows;         /* R >= 0; the gradient: R <= 2^32 - 2               */
+  int64_t n_ids;              /* n >= 0; the gradient: n <= ENGRAM_MAX_EMBED_GRAD_IDS */
+  int64_t table_ld;           /* elements between consecutive rows of the table (or
+                                 of the dense gradient); 0 = dim, else in
+                                 [dim, 2^31 - 1]                                   */
+  int64_t out_ld;             /* the same for out and d_out                        */
+  int32_t dim;                /* D, values per row; 1 <= D <= ENGRAM_MAX_EMBED_DIM  */
+  int32_t table_type;         /* engram_float_type of the table                    */
+  int32_t out_type;           /* engram_float_type of out and d_out                */
+  float scale;                /* finite                                            */
+} engram_embed_desc;
+
 /* Message for a status code (static storage). */
 const char *engram_status_string(int status);
 
@@ -190,10 +222,11 @@ const char *engram_status_string(int status);
  * is the library's only state; it is per thread and never cleared. */
 const char *engram_last_hip_error(void);
 
-/* sizeof the two structs as this library was built, for bindings to check. */
+/* sizeof the structs as this library was built, for bindings to check. */
 size_t engram_sizeof_hash_params(void);
 size_t engram_sizeof_forward_desc(void);
 size_t engram_sizeof_short_conv(void);
+size_t engram_sizeof_embed_desc(void);
 
 /*
  * [host] Segment sizes and offsets: the first `count` primes >= base, in
@@ -635,6 +668,114 @@ int engram_forward_conv(const engram_hash_params *params, const engram_forward_d
                         const void *wkv, const float *q_w, const float *k_w, void *h,
                         float *gate_out, void *workspace, size_t workspace_bytes,
                         hipStream_t stream);
+
+/*
+ * Table lookup with scaling: out[i] = scale * table[row_ids[i]], for tables held
+ * in bf16 or fp32 (a master copy in training, a word embedding).
+ *   table    table_type [table_rows, dim], rows table_ld elements apart, in device
+ *            memory or in pinned host memory (see "Host-resident tables")
+ *   row_ids  int64 [n_ids]; an id outside [0, table_rows) gives a zero row
+ *   out      out_type [n_ids, dim], rows out_ld elements apart; the gaps between
+ *            rows are not written
+ * The product is formed in fp32 and rounded once to out_type (nearest, ties to
+ * even). Rows of a multiple of 8 values at strides that are multiples of 8 move
+ * in 16-byte accesses, others value by value.
+ * Errors: ENGRAM_EINVAL (also: scale not finite, unknown type), ENGRAM_ESHAPE,
+ * ENGRAM_EHIP.
+ */
+int engram_embed(const engram_embed_desc *desc, const void *table, const int64_t *row_ids,
+                 void *out, hipStream_t stream);
+
+/*
+ * Gradient of engram_embed with respect to the table, by sorted row ids: for every
+ * row r that an id names, sum_{i: row_ids[i] = r} scale * d_out[i], summed in fp32 in
+ * an order that depends on the call's sizes and ids only (no floating-point
+ * atomics: the same call gives the same bits). Ids outside [0, table_rows)
+ * contribute nothing.
+ *
+ * engram_embed_grad: the touched rows alone, for tables whose dense gradient would
+ * not fit.
+ *   desc        of the lookup; table_type and table_ld are checked, without effect
+ *   d_out       out_type [n_ids, dim], rows out_ld apart
+ *   row_ids     int64 [n_ids], device memory
+ *   grad_rows   int64 [n_ids]: the touched rows in ascending order, then -1
+ *   grad        float [n_ids, dim], 16-byte aligned: row u is the gradient of table
+ *               row grad_rows[u]; rows from n_rows on are left as they were
+ *   n_rows      int64 [1], device memory: how many rows were touched
+ *   workspace   device, >= engram_embed_grad_workspace_size bytes, 256-byte aligned;
+ *               contents are scratch
+ *
+ * engram_embed_grad_dense: into an array of the table's shape.
+ *   grad        float [table_rows, dim], rows desc->table_ld apart, 16-byte aligned
+ *   accumulate  0: grad is overwritten (zeros in untouched rows, the gaps between
+ *               rows left as they were); 1: the sums are added to grad, untouched
+ *               rows are neither read nor written
+ *   workspace   as above
+ * d_out, grad and the workspace must not overlap.
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
+ */
+size_t engram_embed_grad_workspace_size(const engram_embed_desc *desc);
+int engram_embed_grad(const engram_embed_desc *desc, const void *d_out, const int64_t *row_ids,
+                      int64_t *grad_rows, float *grad, int64_t *n_rows, void *workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+int engram_embed_grad_dense(const engram_embed_desc *desc, const void *d_out,
+                            const int64_t *row_ids, float *grad, int32_t accumulate,
+                            void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Quantisation to 4-bit block floating point (OCP Microscaling Formats 1.0, MXFP4):
+ * per 32 consecutive values of a row one E8M0 scale 2^e with
+ * e = max(floor(log2 max|x|) - 2, -127) and 32 E2M1 codes, the nearest of
+ * {0, 0.5, 1, 1.5, 2, 3, 4, 6} to |x| / 2^e (ties to the even code, above 6: 6) with
+ * x's sign. A block that holds an infinity or a NaN gets scale 0xFF (NaN) and zero
+ * codes.
+ *   src       src_type [rows, cols], rows src_ld elements apart (0 = cols, else
+ *             >= cols); 16-byte aligned. Rows at multiples of 8 are read in 16-byte
+ *             accesses
+ *   out_cols  columns written, a multiple of 32 and >= cols, at most 2^20:
+ *             engram_project_mx4 takes multiples of 128. Columns from cols on count
+ *             as zeros
+ *   codes     uint8 [rows, out_cols / 2], 16-byte aligned
+ *   scales    uint8 [rows, out_cols / 32], 4-byte aligned
+ *   values    NULL, or src_type [rows, cols] with src's strides: the values the
+ *             codes stand for (exact in either type; NaN in a NaN block), for
+ *             quantisation-aware training; may be src itself
+ * rows <= 2^31 - 1 and rows * out_cols <= 2^40.
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EHIP.
+ */
+int engram_quantize_mx4(const void *src, int32_t src_type, int64_t rows, int64_t cols,
+                        int64_t src_ld, int64_t out_cols, void *codes, void *scales,
+                        void *values, hipStream_t stream);
+
+/*
+ * Step 4 with a 4-bit weight: kv[t, c] = sum_k e[t, k] W[c, k] over block-scaled
+ * operands, products exact, fp32 accumulation in gfx950's block-scaled MFMA, rounded
+ * once to bf16 nearest-even. A NaN scale makes its row's outputs NaN. With an E4M3
+ * operand the instruction adds the products of eight consecutive inputs in fixed
+ * point and drops what lies below 2^-13 of the largest (as engram_project_mx does);
+ * with E2M1 operands nothing is dropped.
+ *   e_format  ENGRAM_MX_E4M3: the looked-up rows (engram_gather_mx's codes and
+ *             scales); ENGRAM_MX_E2M1: engram_quantize_mx4's
+ *   e_codes   uint8 [tokens, in_dim] or [tokens, in_dim / 2], 16-byte aligned
+ *   e_scales  uint8 [tokens, in_dim / 32], 4-byte aligned
+ *   w_codes   uint8 [out_dim, in_dim / 2], 16-byte aligned (engram_quantize_mx4)
+ *   w_scales  uint8 [out_dim, in_dim / 32], 4-byte aligned
+ *   kv        bf16 [tokens, out_dim], 16-byte aligned
+ *   in_dim    a multiple of 128, at most 2^20; out_dim % 8 == 0; the tile bound of
+ *             engram_project
+ *   workspace NULL, or at least engram_project_mx4_workspace_size bytes, 256-byte
+ *             aligned; contents are scratch
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
+ */
+int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_format,
+                       const void *w_codes, const void *w_scales, void *kv, int64_t tokens,
+                       int64_t in_dim, int64_t out_dim, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
+/* [host] Bytes of workspace engram_project_mx4 uses (0 if none, on bad arguments or
+ * on a HIP error). */
+size_t engram_project_mx4_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim,
+                                         int32_t e_format);
 
 #ifdef __cplusplus
 }
