@@ -160,6 +160,218 @@ __global__ __launch_bounds__(kThinWaves * 64) void mx4_thin_kernel(Mx4Operands o
   }
 }
 
+// ---- many tokens: 256 x 256 tiles through LDS ---------------------------------------
+// gemm_mx_kernel's tiles and two-stage schedule on the narrower operands. A K-step
+// is 128 bytes of an e row: 256 inputs of E2M1 or 128 of E4M3, and 128 or 64 bytes of
+// a W row. Both operands go global -> LDS by direct loads; 16-byte chunk c of a row
+// sits in slot c ^ f(row), so the 8 rows a quarter-wave reads fall into 8 different
+// slots of 128 bytes. Scales come for two K-steps at once (16 or 8 bytes of a row, half
+// as many cache lines as one step at a time) and are kept in registers.
+template <int EF>
+struct WideCfg {
+  static constexpr int kStep = EF == kFp4 ? 256 : 128;      // inputs of a K-step
+  static constexpr int kSub = kStep / 64;                   // MFMAs along K
+  static constexpr int kWRow = kStep / 2;                   // bytes of a W row
+  static constexpr int kERow = 128;                         // bytes of an e row
+  static constexpr int kSc = kStep / 32;                    // scale bytes of a row
+};
+
+template <int EF>
+struct WideLds {
+  uint8_t w[2][BN * WideCfg<EF>::kWRow];
+  uint8_t e[2][BM * WideCfg<EF>::kERow];
+  uint8_t s[(BN + BM) * 2 * WideCfg<EF>::kSc];              // W rows, then e rows
+};
+
+// K-steps [ks, ke) of the tile at (m0, n0) into acc (zeroed by the caller).
+template <int EF>
+__device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int n0, int ks, int ke,
+                                              f32x16 (&acc)[4][4], uint8_t *__restrict__ w0,
+                                              uint8_t *__restrict__ w1, uint8_t *__restrict__ e0,
+                                              uint8_t *__restrict__ e1, uint8_t *__restrict__ sc) {
+  using Cfg = WideCfg<EF>;
+  constexpr int kSub = Cfg::kSub, kWRow = Cfg::kWRow, kSc = Cfg::kSc;
+  constexpr int kWLoads = BN * kWRow / 1024 / 4;            // direct loads of a wave and step
+  constexpr int kSLoads = (BN + BM) * 2 * kSc / 256 / 4;    // of a wave and two steps
+  const int KB = op.K / 32;
+  const int w_ld = op.K / 2, e_ld = EF == kFp4 ? op.K / 2 : op.K;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave >> 1, wm = wave & 1;
+  const int rows_w = min(BN, op.N - n0), rows_e = min(BM, op.M - m0);
+  const __amdgpu_buffer_rsrc_t rsW = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.w_codes + (int64_t)n0 * w_ld), 0, rows_w * w_ld, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsE = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.e_codes + (int64_t)m0 * e_ld), 0, rows_e * e_ld, kBufferFlags);
+  // waves 0 and 1 load W's scales, 2 and 3 e's
+  const __amdgpu_buffer_rsrc_t rsS =
+      wave < 2 ? __builtin_amdgcn_make_buffer_rsrc(
+                     const_cast<uint8_t *>(op.w_scales + (int64_t)n0 * KB), 0, rows_w * KB, kBufferFlags)
+               : __builtin_amdgcn_make_buffer_rsrc(
+                     const_cast<uint8_t *>(op.e_scales + (int64_t)m0 * KB), 0, rows_e * KB, kBufferFlags);
+  // Direct load i of a wave fills 1 KB: 8 rows of 128 bytes (lane p: row p / 8, slot
+  // p % 8) or 16 rows of 64 (row p / 4, slot p % 4).
+  const int dl_c = (lane & 7) ^ (lane >> 3);
+  const int dl_row = wave * 64 + (lane >> 3);
+  const int e_v0 = dl_row * e_ld + dl_c * 16, e_v1 = dl_row * e_ld + (dl_c ^ 1) * 16;
+  const int w_v0 = EF == kFp4 ? dl_row * w_ld + dl_c * 16
+                              : (wave * 64 + (lane >> 2)) * w_ld + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  const int w_v1 = EF == kFp4 ? dl_row * w_ld + (dl_c ^ 1) * 16 : w_v0;
+  constexpr int kWInstRows = EF == kFp4 ? 8 : 16;
+  // scale dword q of a row: 2 kSc / 4 dwords a row, 256 / (2 kSc) rows an instruction
+  constexpr int kSRows = 256 / (2 * kSc);
+  const int s_v = ((wave & 1) * 128 + lane / (64 / kSRows)) * KB + (lane % (64 / kSRows)) * 4;
+
+  const int frow = lane & 31, h = lane >> 5;
+  const int fsw = (frow & 7) ^ ((frow >> 3) & 1);
+  const int a_base = (wn * 128 + frow) * kWRow, b_base = (wm * 128 + frow) * Cfg::kERow;
+  const int a_sw = EF == kFp4 ? fsw : (frow >> 1) & 3;
+  const int as_base = (wn * 128 + frow) * 2 * kSc + h * (kSc / 2);
+  const int bs_base = (BN + wm * 128 + frow) * 2 * kSc + h * (kSc / 2);
+
+#define M4_W(st) ((st) ? w1 : w0)
+#define M4_E(st) ((st) ? e1 : e0)
+#define M4_LDS(p) ((__attribute__((address_space(3))) void *)(p))
+#define M4_LOADW(kt_, st, i)                                                                   \
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsW, M4_LDS(&M4_W(st)[(wave * kWLoads + (i)) * 1024]), 16, \
+                                           ((i) & 1) ? w_v1 : w_v0,                            \
+                                           (i) * kWInstRows * w_ld + (kt_) * kWRow, 0, 0);
+#define M4_LOADE(kt_, st, i)                                                                   \
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsE, M4_LDS(&M4_E(st)[(wave * 8 + (i)) * 1024]), 16, \
+                                           ((i) & 1) ? e_v1 : e_v0,                            \
+                                           (i) * 8 * e_ld + (kt_) * Cfg::kERow, 0, 0);
+// the scales of steps kt_ and kt_ + 1 (kt_ - ks even)
+#define M4_LOADS(kt_)                                                                          \
+  _Pragma("unroll") for (int i = 0; i < kSLoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
+      rsS, M4_LDS(&sc[(wave * kSLoads + i) * 256]), 4, s_v, i * kSRows * KB + (kt_) * kSc, 0, 0);
+#define M4_LOADSTEP(kt_, st)                                                                   \
+  _Pragma("unroll") for (int i = 0; i < kWLoads; ++i) { M4_LOADW(kt_, st, i) }                 \
+  _Pragma("unroll") for (int i = 0; i < 8; ++i) { M4_LOADE(kt_, st, i) }
+#define M4_CHUNK(buf, base, c, sw) \
+  (*reinterpret_cast<const uint4 *>(&(buf)[(base) + (((c) ^ (sw)) << 4)]))
+#define M4_FRAGS(st, s, fa, fb)                                                                \
+  _Pragma("unroll") for (int i = 0; i < 4; ++i)                                                \
+    fa[i] = fp4_operand(M4_CHUNK(M4_W(st), a_base + i * 32 * kWRow, kSub * h + (s), a_sw));    \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j)                                                \
+    fb[j] = EF == kFp4                                                                         \
+                ? fp4_operand(M4_CHUNK(M4_E(st), b_base + j * 32 * 128, kSub * h + (s), fsw))  \
+                : fp8_operand(M4_CHUNK(M4_E(st), b_base + j * 32 * 128, 2 * (s) + h, fsw),     \
+                              M4_CHUNK(M4_E(st), b_base + j * 32 * 128, 2 * (kSub + (s)) + h, fsw));
+  // this lane's scales of step q (0 or 1) of a pair, as the low bytes of a word
+  auto scale_word = [&](int base, int q) -> uint32_t {
+    const uint8_t *p = &sc[base + q * kSc];
+    return EF == kFp4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
+  };
+#define M4_SCALES(q, sA, sB)                                                                   \
+  _Pragma("unroll") for (int i = 0; i < 4; ++i) sA[i] = scale_word(as_base + i * 32 * 2 * kSc, q); \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j) sB[j] = scale_word(bs_base + j * 32 * 2 * kSc, q);
+#define M4_MFMA(s, fa, fb, sA, sB)                                                             \
+  _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
+    acc[i][j] = mfma_unit<EF, s>(fa[i], fb[j], acc[i][j], sA[i], sB[j]);
+#define M4_BARRIER() asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory")
+// E2M1, in_dim an odd multiple of 128: the last step's upper four blocks lie in the
+// next row. Scales of 2^-127 on both sides take their products below the smallest
+// fp32, to zero.
+#define M4_TAIL(kt_, sA, sB)                                                                   \
+  if (EF == kFp4 && ((kt_) + 1) * 8 > KB && h) {                                               \
+    _Pragma("unroll") for (int i = 0; i < 4; ++i) { sA[i] = 0u; sB[i] = 0u; }                  \
+  }
+
+  i32x8 fa0[4], fb0[4], fa1[4], fb1[4];
+  uint32_t sA0[4], sB0[4], sA1[4], sB1[4];
+  __syncthreads();
+  M4_LOADS(ks)
+  M4_LOADSTEP(ks, 0)
+  M4_LOADSTEP(ks + 1, 1)
+  M4_BARRIER();
+  M4_FRAGS(0, 0, fa0, fb0)
+  M4_SCALES(0, sA0, sB0)
+  M4_SCALES(1, sA1, sB1)
+// One step from stage P: its last fragments are read before the barrier, the next
+// step's first ones (stage Q) behind it, while stage P takes step kt + 2. The LDS
+// reads come before the new direct loads: the compiler, which cannot see the wait
+// inside the barrier, puts a full vmcnt wait before them.
+#define M4_STEP(kt_, P, Q, sA, sB, READ, LOAD)                                                     \
+  {                                                                                            \
+    M4_TAIL(kt_, sA, sB)                                                                       \
+    if constexpr (kSub == 4) {                                                                 \
+      M4_FRAGS(P, 1, fa1, fb1)                                                                 \
+      M4_MFMA(0, fa0, fb0, sA, sB)                                                             \
+      M4_FRAGS(P, 2, fa0, fb0)                                                                 \
+      M4_MFMA(1, fa1, fb1, sA, sB)                                                             \
+      M4_FRAGS(P, 3, fa1, fb1)                                                                 \
+      M4_MFMA(2, fa0, fb0, sA, sB)                                                             \
+    } else {                                                                                   \
+      M4_FRAGS(P, 1, fa1, fb1)                                                                 \
+      M4_MFMA(0, fa0, fb0, sA, sB)                                                             \
+    }                                                                                          \
+    M4_BARRIER();                                                                              \
+    M4_FRAGS(Q, 0, fa0, fb0)                                                                   \
+    READ                                                                                       \
+    M4_LOADSTEP((kt_) + 2, P)                                                                  \
+    LOAD                                                                                       \
+    M4_MFMA((kSub - 1), fa1, fb1, sA, sB)                                                      \
+  }
+  int kt = ks;
+  for (; kt + 1 < ke; kt += 2) {
+    M4_STEP(kt, 0, 1, sA0, sB0, , M4_LOADS(kt + 2))
+    uint32_t tA[4], tB[4];
+    M4_STEP(kt + 1, 1, 0, sA1, sB1, M4_SCALES(0, sA0, sB0) M4_SCALES(1, tA, tB), )
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sA1[i] = tA[i];
+      sB1[i] = tB[i];
+    }
+  }
+  if (kt < ke) M4_STEP(kt, 0, 1, sA0, sB0, , )
+  // direct loads issued for steps past ke land before the stages are reused
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#undef M4_STEP
+#undef M4_TAIL
+#undef M4_BARRIER
+#undef M4_MFMA
+#undef M4_SCALES
+#undef M4_FRAGS
+#undef M4_CHUNK
+#undef M4_LOADSTEP
+#undef M4_LOADS
+#undef M4_LOADE
+#undef M4_LOADW
+#undef M4_LDS
+#undef M4_E
+#undef M4_W
+}
+
+template <int EF>
+__global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int tiles_n) {
+  __shared__ __align__(1024) WideLds<EF> lds;
+  int m0, n0;
+  tile_origin(tiles_m, tiles_n, BN, m0, n0);
+  f32x16 acc[4][4];
+  zero_acc(acc);
+  wide_tile_mx4<EF>(op, m0, n0, 0, (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep, acc, lds.w[0],
+                    lds.w[1], lds.e[0], lds.e[1], lds.s);
+  wide_store_bf16(acc, kv, op.M, op.N, m0, n0);
+}
+
+template <int EF>
+hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
+  if (op.M > 64) {
+    const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
+    hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kWideThreads), 0,
+                       stream, op, kv, tiles_m, tiles_n);
+    return hipGetLastError();
+  }
+  const dim3 block(kThinWaves * 64);
+  if (op.M <= 32)
+    hipLaunchKernelGGL((mx4_thin_kernel<EF, 1>), dim3((unsigned)((op.N + 31) / 32)), block, 0, stream, op, kv);
+  else
+    hipLaunchKernelGGL((mx4_thin_kernel<EF, 2>), dim3((unsigned)((op.N + 31) / 32)), block, 0, stream, op, kv);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t engram_gemm_mx4_workspace(int64_t m, int64_t n, int64_t k, bool e_fp4, size_t *bytes) {
@@ -175,11 +387,5 @@ hipError_t engram_launch_gemm_mx4(const uint8_t *w_codes, const uint8_t *w_scale
   (void)workspace; (void)workspace_bytes;
   if (m <= 0 || n <= 0) return hipSuccess;
   const Mx4Operands op{w_codes, w_scales, e_codes, e_scales, (int)m, (int)n, (int)k};
-  const dim3 block(kThinWaves * 64);
-  const dim3 grid((unsigned)((n + 31) / 32), (unsigned)((m + 63) / 64));
-  if (e_fp4)
-    hipLaunchKernelGGL((mx4_thin_kernel<kFp4, 2>), grid, block, 0, stream, op, kv);
-  else
-    hipLaunchKernelGGL((mx4_thin_kernel<kFp8, 2>), grid, block, 0, stream, op, kv);
-  return hipGetLastError();
+  return e_fp4 ? launch_mx4<kFp4>(op, kv, stream) : launch_mx4<kFp8>(op, kv, stream);
 }
