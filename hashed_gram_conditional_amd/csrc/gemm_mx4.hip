@@ -176,12 +176,14 @@ struct WideCfg {
   static constexpr int kSc = kStep / 32;                    // scale bytes of a row
 };
 
-template <int EF>
-struct WideLds {
-  uint8_t w[2][BN * WideCfg<EF>::kWRow];
-  uint8_t e[2][BM * WideCfg<EF>::kERow];
-  uint8_t s[(BN + BM) * 2 * WideCfg<EF>::kSc];              // W rows, then e rows
-};
+// The stages are separate LDS variables: the compiler then knows that direct loads
+// into one and reads of another do not meet, and waits for nothing in between.
+#define ENGRAM_MX4_WIDE_LDS(EF)                                                                \
+  __shared__ __align__(1024) uint8_t w0[BN * WideCfg<EF>::kWRow];                              \
+  __shared__ __align__(1024) uint8_t w1[BN * WideCfg<EF>::kWRow];                              \
+  __shared__ __align__(1024) uint8_t e0[BM * WideCfg<EF>::kERow];                              \
+  __shared__ __align__(1024) uint8_t e1[BM * WideCfg<EF>::kERow];                              \
+  __shared__ __align__(1024) uint8_t sc[(BN + BM) * 2 * WideCfg<EF>::kSc] /* W rows, then e rows */
 
 // K-steps [ks, ke) of the tile at (m0, n0) into acc (zeroed by the caller).
 template <int EF>
@@ -193,6 +195,7 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
   constexpr int kSub = Cfg::kSub, kWRow = Cfg::kWRow, kSc = Cfg::kSc;
   constexpr int kWLoads = BN * kWRow / 1024 / 4;            // direct loads of a wave and step
   constexpr int kSLoads = (BN + BM) * 2 * kSc / 256 / 4;    // of a wave and two steps
+  constexpr int kReads = EF == kFp4 ? 8 : 12;               // LDS reads of one set of fragments
   const int KB = op.K / 32;
   const int w_ld = op.K / 2, e_ld = EF == kFp4 ? op.K / 2 : op.K;
   const int tid = threadIdx.x;
@@ -258,14 +261,13 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
                 ? fp4_operand(M4_CHUNK(M4_E(st), b_base + j * 32 * 128, kSub * h + (s), fsw))  \
                 : fp8_operand(M4_CHUNK(M4_E(st), b_base + j * 32 * 128, 2 * (s) + h, fsw),     \
                               M4_CHUNK(M4_E(st), b_base + j * 32 * 128, 2 * (kSub + (s)) + h, fsw));
-  // this lane's scales of step q (0 or 1) of a pair, as the low bytes of a word
-  auto scale_word = [&](int base, int q) -> uint32_t {
-    const uint8_t *p = &sc[base + q * kSc];
-    return EF == kFp4 ? *reinterpret_cast<const uint32_t *>(p) : *reinterpret_cast<const uint16_t *>(p);
-  };
+// this lane's scales of step q (0 or 1) of a pair, as the low bytes of a word
+#define M4_SCALE(base, q)                                                                      \
+  (EF == kFp4 ? *reinterpret_cast<const uint32_t *>(&sc[(base) + (q) * kSc])                   \
+              : (uint32_t)*reinterpret_cast<const uint16_t *>(&sc[(base) + (q) * kSc]))
 #define M4_SCALES(q, sA, sB)                                                                   \
-  _Pragma("unroll") for (int i = 0; i < 4; ++i) sA[i] = scale_word(as_base + i * 32 * 2 * kSc, q); \
-  _Pragma("unroll") for (int j = 0; j < 4; ++j) sB[j] = scale_word(bs_base + j * 32 * 2 * kSc, q);
+  _Pragma("unroll") for (int i = 0; i < 4; ++i) sA[i] = M4_SCALE(as_base + i * 32 * 2 * kSc, q); \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j) sB[j] = M4_SCALE(bs_base + j * 32 * 2 * kSc, q);
 #define M4_MFMA(s, fa, fb, sA, sB)                                                             \
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = mfma_unit<EF, s>(fa[i], fb[j], acc[i][j], sA[i], sB[j]);
@@ -274,8 +276,9 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 // next row. Scales of 2^-127 on both sides take their products below the smallest
 // fp32, to zero.
 #define M4_TAIL(kt_, sA, sB)                                                                   \
-  if (EF == kFp4 && ((kt_) + 1) * 8 > KB && h) {                                               \
-    _Pragma("unroll") for (int i = 0; i < 4; ++i) { sA[i] = 0u; sB[i] = 0u; }                  \
+  if constexpr (EF == kFp4) {                                                                  \
+    const uint32_t keep = ((kt_) + 1) * 8 > KB && h ? 0u : ~0u;                                \
+    _Pragma("unroll") for (int i = 0; i < 4; ++i) { sA[i] &= keep; sB[i] &= keep; }            \
   }
 
   i32x8 fa0[4], fb0[4], fa1[4], fb1[4];
@@ -292,26 +295,35 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 // step's first ones (stage Q) behind it, while stage P takes step kt + 2. The LDS
 // reads come before the new direct loads: the compiler, which cannot see the wait
 // inside the barrier, puts a full vmcnt wait before them.
-#define M4_STEP(kt_, P, Q, sA, sB, READ, LOAD)                                                     \
+#define M4_FENCE() __builtin_amdgcn_sched_barrier(0)
+#define M4_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier(mask, n, 0)
+// 16 MFMAs with the next fragments' reads between the first of them
+#define M4_PART(P, s, ra, rb, fa, fb, sA, sB)                                                  \
+  M4_FRAGS(P, (s) + 1, ra, rb)                                                                 \
+  M4_MFMA(s, fa, fb, sA, sB)                                                                   \
+  _Pragma("unroll") for (int g_ = 0; g_ < kReads; ++g_) { M4_GROUP(0x100, 1); M4_GROUP(0x008, 1); } \
+  M4_FENCE();
+#define M4_STEP(kt_, P, Q, sA, sB, READ, LOAD)                                                 \
   {                                                                                            \
     M4_TAIL(kt_, sA, sB)                                                                       \
     if constexpr (kSub == 4) {                                                                 \
-      M4_FRAGS(P, 1, fa1, fb1)                                                                 \
-      M4_MFMA(0, fa0, fb0, sA, sB)                                                             \
-      M4_FRAGS(P, 2, fa0, fb0)                                                                 \
-      M4_MFMA(1, fa1, fb1, sA, sB)                                                             \
-      M4_FRAGS(P, 3, fa1, fb1)                                                                 \
-      M4_MFMA(2, fa0, fb0, sA, sB)                                                             \
+      M4_PART(P, 0, fa1, fb1, fa0, fb0, sA, sB)                                                \
+      M4_PART(P, 1, fa0, fb0, fa1, fb1, sA, sB)                                                \
+      M4_PART(P, 2, fa1, fb1, fa0, fb0, sA, sB)                                                \
     } else {                                                                                   \
-      M4_FRAGS(P, 1, fa1, fb1)                                                                 \
-      M4_MFMA(0, fa0, fb0, sA, sB)                                                             \
+      M4_PART(P, 0, fa1, fb1, fa0, fb0, sA, sB)                                                \
     }                                                                                          \
     M4_BARRIER();                                                                              \
+    M4_FENCE();                                                                                \
     M4_FRAGS(Q, 0, fa0, fb0)                                                                   \
     READ                                                                                       \
     M4_LOADSTEP((kt_) + 2, P)                                                                  \
     LOAD                                                                                       \
     M4_MFMA((kSub - 1), fa1, fb1, sA, sB)                                                      \
+    _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                        \
+      M4_GROUP(0x008, 1); M4_GROUP(0x100, 2); M4_GROUP(0x020, 2);                              \
+    }                                                                                          \
+    M4_FENCE();                                                                                \
   }
   int kt = ks;
   for (; kt + 1 < ke; kt += 2) {
@@ -328,10 +340,14 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
   // direct loads issued for steps past ke land before the stages are reused
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #undef M4_STEP
+#undef M4_PART
+#undef M4_GROUP
+#undef M4_FENCE
 #undef M4_TAIL
 #undef M4_BARRIER
 #undef M4_MFMA
 #undef M4_SCALES
+#undef M4_SCALE
 #undef M4_FRAGS
 #undef M4_CHUNK
 #undef M4_LOADSTEP
@@ -346,13 +362,13 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 template <int EF>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int tiles_n) {
-  __shared__ __align__(1024) WideLds<EF> lds;
+  ENGRAM_MX4_WIDE_LDS(EF);
   int m0, n0;
   tile_origin(tiles_m, tiles_n, BN, m0, n0);
   f32x16 acc[4][4];
   zero_acc(acc);
-  wide_tile_mx4<EF>(op, m0, n0, 0, (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep, acc, lds.w[0],
-                    lds.w[1], lds.e[0], lds.e[1], lds.s);
+  wide_tile_mx4<EF>(op, m0, n0, 0, (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep, acc, w0,
+                    w1, e0, e1, sc);
   wide_store_bf16(acc, kv, op.M, op.N, m0, n0);
 }
 
