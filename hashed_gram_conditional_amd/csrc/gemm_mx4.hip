@@ -359,6 +359,40 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 #undef M4_W
 }
 
+// bf16 store of a finished tile in whole cache lines. A lane's accumulators are 4
+// columns of one token at a time, 16 bytes of a line with its partner's: stored from
+// the registers, a tile's 128 KB took 4 times as many write transactions as lines.
+// Each wave passes 32 tokens x 128 columns at a time through 8 KB of LDS (chunk c of
+// token t in slot c ^ t % 16) and stores 256 bytes of a token with 16 lanes.
+__device__ __forceinline__ void wide_store_lines(const f32x16 (&acc)[4][4], uint16_t *__restrict__ kv,
+                                                 int M, int N, int m0, int n0, uint8_t *buf) {
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int wn = wave >> 1, wm = wave & 1;
+  const int frow = lane & 31, fk = lane >> 5;
+  uint8_t *mine = buf + wave * 8192;
+  const int col = n0 + wn * 128 + (lane & 15) * 8;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint2 v;
+        v.x = engram::pack_bf16x2(acc[i][j][g * 4 + 0], acc[i][j][g * 4 + 1]);
+        v.y = engram::pack_bf16x2(acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]);
+        *reinterpret_cast<uint2 *>(mine + frow * 256 + (((i * 4 + g) ^ (frow & 15)) << 4) + fk * 8) = v;
+      }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int t = q * 4 + (lane >> 4);
+      const uint4 v = *reinterpret_cast<const uint4 *>(mine + t * 256 + (((lane & 15) ^ (t & 15)) << 4));
+      const int m = m0 + wm * 128 + j * 32 + t;
+      if (m < M && col < N) *reinterpret_cast<uint4 *>(kv + (int64_t)m * N + col) = v;
+    }
+  }
+}
+
 template <int EF>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int tiles_n) {
@@ -369,7 +403,8 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
   zero_acc(acc);
   wide_tile_mx4<EF>(op, m0, n0, 0, (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep, acc, w0,
                     w1, e0, e1, sc);
-  wide_store_bf16(acc, kv, op.M, op.N, m0, n0);
+  __syncthreads();                    // every wave is done with the stages
+  wide_store_lines(acc, kv, op.M, op.N, m0, n0, e0);
 }
 
 template <int EF>
