@@ -363,7 +363,9 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 // columns of one token at a time, 16 bytes of a line with its partner's: stored from
 // the registers, a tile's 128 KB took 4 times as many write transactions as lines.
 // Each wave passes 32 tokens x 128 columns at a time through 8 KB of LDS (chunk c of
-// token t in slot c ^ t % 16) and stores 256 bytes of a token with 16 lanes.
+// token t in slot c ^ t % 16) and stores 256 bytes of a token with 16 lanes. The
+// stores are marked nontemporal, so that kv does not push the operands' panels out of
+// L2 (2.83 -> 2.57 ms at 32768 x 6144 x 25600).
 __device__ __forceinline__ void wide_store_lines(const f32x16 (&acc)[4][4], uint16_t *__restrict__ kv,
                                                  int M, int N, int m0, int n0, uint8_t *buf) {
   const int lane = threadIdx.x & 63;
@@ -386,9 +388,10 @@ __device__ __forceinline__ void wide_store_lines(const f32x16 (&acc)[4][4], uint
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int t = q * 4 + (lane >> 4);
-      const uint4 v = *reinterpret_cast<const uint4 *>(mine + t * 256 + (((lane & 15) ^ (t & 15)) << 4));
+      const engram::u32x4 v = *reinterpret_cast<const engram::u32x4 *>(mine + t * 256 + (((lane & 15) ^ (t & 15)) << 4));
       const int m = m0 + wm * 128 + j * 32 + t;
-      if (m < M && col < N) *reinterpret_cast<uint4 *>(kv + (int64_t)m * N + col) = v;
+      if (m < M && col < N)
+        __builtin_nontemporal_store(v, reinterpret_cast<engram::u32x4 *>(kv + (int64_t)m * N + col));
     }
   }
 }
