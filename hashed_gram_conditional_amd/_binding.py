@@ -215,8 +215,12 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        # torch.cuda.current_stream() builds a Stream object (2.9 us a call, against
+        # 0.2 us for its handle alone and 4 us for a whole small entry point)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
