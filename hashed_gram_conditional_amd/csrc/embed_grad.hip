@@ -3,17 +3,19 @@
 // same call gives the same bits.
 //
 //   1. Keys: the row id, or table_rows for an id outside the table (those sort
-//      behind every row and are dropped). A stable least-digit radix sort of
-//      (key, i) puts each row's occurrences side by side in the order of i.
-//      Up to kSmall ids one block sorts in LDS; above, each pass is a
-//      histogram per block, a scan per digit and a scatter.
+//      behind every row and are dropped). A stable sort of (key, i) puts each
+//      row's occurrences side by side in the order of i. Up to kSmall ids blocks
+//      of kPart are sorted in LDS and merged by rank: an element's place is its
+//      place in its own part plus, for every other part, a binary search. Above,
+//      a least-digit radix sort: each pass is a histogram per block, a scan per
+//      digit and a scatter.
 //   2. Runs of equal keys: run u starts at sorted position starts[u]; the number
 //      of runs is known only on the device.
 //   3. Sums: the sorted positions are cut into chunks of `chunk`; a thread owns
 //      one chunk and 8 (bf16) or 4 (fp32) columns, so neighbouring threads read
 //      whole rows, and walks the runs that begin in its chunk, adding in fp32 in
-//      the order of i. A run longer than kLong is summed piece by piece, a piece
-//      per chunk it touches, and
+//      the order of i. A run longer than `longest` is summed piece by piece, a
+//      piece per chunk it touches, and
 //   4. the pieces are joined: fixed groups of pieces in order, then the groups
 //      in order.
 //
@@ -24,21 +26,28 @@
 
 namespace {
 
-constexpr int kSmall = 16384;          // ids one block sorts in LDS
-constexpr int kSmallThreads = 1024;
-constexpr int kSmallItems = kSmall / kSmallThreads;
-constexpr int kSmallBits = 8;
-constexpr int kLong = 64;              // longest run summed by one thread; >= every chunk
+constexpr int kPart = 1024;            // ids a block sorts in LDS
+constexpr int kPartThreads = 256;
+constexpr int kPartItems = kPart / kPartThreads;
+constexpr int kPartBits = 8;
+constexpr int kSmall = 32768;          // ids whose keys one block holds in LDS to merge
+constexpr int kMergeThreads = 1024;
+constexpr int kMergeElems = 64;
+constexpr int kMaxChunk = 64;          // positions of a chunk, at most
 
 constexpr int kSortThreads = 512;
 constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;
-constexpr int kMaxBits = 10;           // digit of one pass of the large sort
-constexpr int kMaxBlocks = 512;        // blocks of one pass
+constexpr int kMaxBits = 11;           // digit of one pass of the large sort
+constexpr int kMaxBlocks = 1024;       // blocks of one pass
+constexpr int kScanThreads = 1024;
+constexpr int kScanDigits = 32;
+constexpr int kRunThreads = 1024;
 
 constexpr int kSumThreads = 256;
-constexpr int kJoinThreads = 1024;
-constexpr int kJoinChunks = 32;        // chunks one join block looks after
+constexpr int kJoinThreads = 512;
+constexpr int kJoinChunks = 8;         // chunks one join block looks after
+constexpr int kFewPieces = 16;         // pieces of a run that one group of threads joins
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t table_rows) {
   return (uint64_t)id < (uint64_t)table_rows ? (uint32_t)id : (uint32_t)table_rows;
@@ -62,6 +71,30 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, int bits) {
 
 __device__ __forceinline__ int lanes_below(uint64_t mask) {
   return __popcll(mask & ((1ull << (threadIdx.x & 63)) - 1ull));
+}
+
+// Ranks of a wave's items among those of equal digit, items in order and lanes in
+// order within an item: rank[i] = how many came before. cnt counts the wave's digits
+// (zeroed before). A wave's LDS operations run in program order, so the counters'
+// additions need no wait between them.
+template <int BITS, int ITEMS, class Digit, class In>
+__device__ __forceinline__ void wave_ranks(uint32_t *cnt, int bits, Digit digit, In in,
+                                           uint32_t (&rank)[ITEMS]) {
+  const int lane = threadIdx.x & 63;
+  uint32_t before[ITEMS];
+  int leader[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t d = digit(i);
+    const bool mine = in(i);
+    const uint64_t mask = same_digit<BITS>(d, bits) & __ballot(mine);
+    leader[i] = mask ? __ffsll((unsigned long long)mask) - 1 : 0;
+    rank[i] = (uint32_t)lanes_below(mask);
+    before[i] = 0;
+    if (mine && lane == leader[i]) before[i] = atomicAdd(&cnt[d], (uint32_t)__popcll(mask));
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) rank[i] += (uint32_t)__shfl((int)before[i], leader[i], engram::kWave);
 }
 
 // Inclusive scan over the wave.
@@ -97,12 +130,12 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *part, uint3
 
 // What the sums need to know of the sorted ids.
 struct Runs {
-  const uint32_t *keys;       // [n] sorted
-  const uint32_t *order;      // [n] the i of each sorted position
+  const uint2 *pairs;         // [n] sorted (key, i)
   uint32_t *starts;           // [n + 1] first position of run u; starts[runs] = ids kept
   uint32_t *chunk_run;        // [chunks] the run that holds a chunk's first position
   uint32_t *meta;             // [0] runs, [1] ids kept
-  int chunk;
+  int chunk, chunk_log2;      // positions of a chunk, a power of two
+  int longest;                // >= chunk
 };
 
 // Where the sums go: rows of fp32, at the run's number (compact) or its row id.
@@ -114,144 +147,202 @@ struct Sums {
   int dense, accumulate;
 };
 
-// Zeroes grad[0 .. rows) x [0 .. dim), groups of 4 or single columns.
-__device__ __forceinline__ void zero_grad(const Sums &s, const EngramFastDiv &groups, int vec,
-                                          int64_t total, int64_t first, int64_t step) {
-  for (int64_t g = first; g < total; g += step) {
-    const int64_t row = groups.div(g);
-    const int64_t col = g - row * groups.d;
-    if (vec)
-      *reinterpret_cast<float4 *>(s.grad + row * s.ld + col * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+// Zeroes grad[0 .. rows) x [0 .. dim): dense rows as one array, else by groups of 4
+// or single columns.
+struct Zero {
+  EngramFastDiv groups;
+  int64_t total;              // groups in all; 0: nothing to do
+  int vec, flat;
+};
+
+__device__ __forceinline__ void zero_grad(const Sums &s, const Zero &z, int64_t first, int64_t step) {
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (z.flat) {
+#pragma unroll 4
+    for (int64_t g = first; g < z.total; g += step) reinterpret_cast<float4 *>(s.grad)[g] = none;
+    return;
+  }
+  for (int64_t g = first; g < z.total; g += step) {
+    const int64_t row = z.groups.div(g);
+    const int64_t col = g - row * z.groups.d;
+    if (z.vec)
+      *reinterpret_cast<float4 *>(s.grad + row * s.ld + col * 4) = none;
     else
       s.grad[row * s.ld + col] = 0.f;
   }
 }
 
-__global__ __launch_bounds__(256) void zero_grad_kernel(Sums s, EngramFastDiv groups, int vec,
-                                                        int64_t total) {
-  zero_grad(s, groups, vec, total, (int64_t)blockIdx.x * 256 + threadIdx.x,
-            (int64_t)gridDim.x * 256);
+__global__ __launch_bounds__(256) void zero_grad_kernel(Sums s, Zero z) {
+  zero_grad(s, z, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
-// Block 0: the whole sort and the runs of up to kSmall ids. The other blocks
-// (a dense gradient that is not added to) clear the gradient meanwhile.
-struct SmallLds {
-  uint32_t key[kSmall];
-  uint16_t idx[kSmall];
-  uint32_t cnt[kSmallThreads / 64][1 << kSmallBits];
-  uint32_t part[17];
-  uint32_t kept;
-};
-
-__global__ __launch_bounds__(kSmallThreads) void small_sort_kernel(
-    const int64_t *__restrict__ ids, int n, int64_t table_rows, int bits, Runs r,
-    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ order_out, Sums s,
-    EngramFastDiv zero_groups, int zero_vec, int64_t zero_total) {
-  __shared__ SmallLds lds;
-  if (blockIdx.x > 0) {
-    zero_grad(s, zero_groups, zero_vec, zero_total,
-              (int64_t)(blockIdx.x - 1) * kSmallThreads + threadIdx.x,
-              (int64_t)(gridDim.x - 1) * kSmallThreads);
+// ---- the sort of up to kSmall ids -------------------------------------------------
+// Block b < parts: a stable radix sort of part b. The other blocks (a dense gradient
+// that is not added to) clear the gradient meanwhile.
+__global__ __launch_bounds__(kPartThreads) void sort_part_kernel(
+    const int64_t *__restrict__ ids, int n, int64_t table_rows, int bits, uint2 *__restrict__ out,
+    int parts, Sums s, Zero z) {
+  constexpr int kWaves = kPartThreads / 64;
+  __shared__ uint32_t keys[kPart];
+  __shared__ uint16_t order[kPart];
+  __shared__ uint32_t cnt[kWaves][1 << kPartBits];
+  __shared__ uint32_t part[17];
+  if ((int)blockIdx.x >= parts) {
+    zero_grad(s, z, (int64_t)(blockIdx.x - parts) * kPartThreads + threadIdx.x,
+              (int64_t)(gridDim.x - parts) * kPartThreads);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int items = (n + kSmallThreads - 1) / kSmallThreads;
-  // item i of the thread is position first + 64 i
-  const int first = wave * 64 * items + lane;
-  for (int p = tid; p < n; p += kSmallThreads) {
-    lds.key[p] = key_of(ids[p], table_rows);
-    lds.idx[p] = (uint16_t)p;
+  const int p0 = blockIdx.x * kPart;
+  const int count = min(kPart, n - p0);
+  // item i of the thread is position first + 64 i of the part
+  const int first = wave * 64 * kPartItems + lane;
+  uint32_t key[kPartItems], rank[kPartItems];
+  uint16_t idx[kPartItems];
+#pragma unroll
+  for (int i = 0; i < kPartItems; ++i) {
+    const int p = first + 64 * i;
+    key[i] = p < count ? key_of(ids[p0 + p], table_rows) : 0u;
+    idx[i] = (uint16_t)p;
   }
-  if (tid == 0) lds.kept = (uint32_t)n;
-  for (int shift = 0; shift < bits; shift += kSmallBits) {
-    for (int d = lane; d < (1 << kSmallBits); d += 64) lds.cnt[wave][d] = 0u;
+  for (int shift = 0; shift < bits; shift += kPartBits) {
+    for (int d = lane; d < (1 << kPartBits); d += 64) cnt[wave][d] = 0u;
     __syncthreads();
-    uint32_t key[kSmallItems], rank[kSmallItems];
-    uint16_t idx[kSmallItems];
+    wave_ranks<kPartBits, kPartItems>(cnt[wave], kPartBits, [&](int i) { return (key[i] >> shift) & ((1u << kPartBits) - 1u); },
+                                      [&](int i) { return first + 64 * i < count; }, rank);
+    __syncthreads();
+    uint32_t c[kWaves], sum = 0, total;      // thread t looks after digit t
 #pragma unroll
-    for (int i = 0; i < kSmallItems; ++i) {
-      if (i < items) {
-        const int p = first + 64 * i;
-        const bool in = p < n;
-        key[i] = in ? lds.key[p] : 0u;
-        idx[i] = in ? lds.idx[p] : (uint16_t)0;
-        const uint32_t d = (key[i] >> shift) & ((1u << kSmallBits) - 1u);
-        const uint64_t mask = same_digit<kSmallBits>(d, kSmallBits) & __ballot(in);
-        uint32_t before = 0;
-        const int leader = mask ? __ffsll((unsigned long long)mask) - 1 : 0;
-        if (in && lane == leader) before = atomicAdd(&lds.cnt[wave][d], (uint32_t)__popcll(mask));
-        rank[i] = (uint32_t)__shfl((int)before, leader, engram::kWave) + (uint32_t)lanes_below(mask);
+    for (int w = 0; w < kWaves; ++w) {
+      c[w] = cnt[w][tid];
+      sum += c[w];
+    }
+    uint32_t base = block_scan(sum, part, total);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      cnt[w][tid] = base;
+      base += c[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPartItems; ++i) {
+      if (first + 64 * i < count) {
+        const uint32_t d = (key[i] >> shift) & ((1u << kPartBits) - 1u);
+        const uint32_t to = cnt[wave][d] + rank[i];
+        keys[to] = key[i];
+        order[to] = idx[i];
       }
     }
     __syncthreads();
-    uint32_t sum = 0;
-    if (tid < (1 << kSmallBits)) {
 #pragma unroll
-      for (int w = 0; w < kSmallThreads / 64; ++w) {
-        const uint32_t c = lds.cnt[w][tid];
-        lds.cnt[w][tid] = sum;
-        sum += c;
+    for (int i = 0; i < kPartItems; ++i) {
+      const int p = first + 64 * i;
+      if (p < count) {
+        key[i] = keys[p];
+        idx[i] = order[p];
       }
     }
-    uint32_t total;
-    const uint32_t base = block_scan(sum, lds.part, total);
-    if (tid < (1 << kSmallBits)) {
+  }
 #pragma unroll
-      for (int w = 0; w < kSmallThreads / 64; ++w) lds.cnt[w][tid] += base;
-    }
-    __syncthreads();
+  for (int i = 0; i < kPartItems; ++i) {
+    const int p = first + 64 * i;
+    if (p < count) out[p0 + p] = make_uint2(key[i], (uint32_t)(p0 + idx[i]));
+  }
+}
+static_assert(kPartThreads == 1 << kPartBits, "one thread per digit");
+
+// Each block places kMergeElems elements of the sorted parts. Thread (q, e) finds how
+// many keys of part q (and of part q + 16) come before element e: an equal key of
+// an earlier part does, one of a later part does not.
+__global__ __launch_bounds__(kMergeThreads) void merge_parts_kernel(const uint2 *__restrict__ in, int n,
+                                                                    uint2 *__restrict__ out) {
+  __shared__ uint32_t keys[kSmall];
+  __shared__ uint32_t place[kMergeElems];
+  const int tid = threadIdx.x;
+  const int e = blockIdx.x * kMergeElems + (tid & (kMergeElems - 1));
+  if (tid < kMergeElems) place[tid] = (uint32_t)(e % kPart);
+#pragma unroll 8
+  for (int p = tid; p < n; p += kMergeThreads) keys[p] = in[p].x;
+  __syncthreads();
+  if (e < n) {
+    const uint32_t key = keys[e];
+    const int mine = e / kPart;
+    const int parts = (n + kPart - 1) / kPart;
+    uint32_t before = 0;
+    for (int q = tid / kMergeElems; q < parts; q += kMergeThreads / kMergeElems) {
+      if (q == mine) continue;
+      const uint32_t *k = keys + q * kPart;
+      const int count = min(kPart, n - q * kPart);
+      const uint32_t bound = key + (q < mine ? 1u : 0u);
+      int at = 0;
 #pragma unroll
-    for (int i = 0; i < kSmallItems; ++i) {
-      if (i < items && first + 64 * i < n) {
-        const uint32_t d = (key[i] >> shift) & ((1u << kSmallBits) - 1u);
-        const uint32_t to = lds.cnt[wave][d] + rank[i];
-        lds.key[to] = key[i];
-        lds.idx[to] = idx[i];
-      }
+      for (int step = kPart / 2; step > 0; step >>= 1)
+        if (at + step <= count && k[at + step - 1] < bound) at += step;
+      if (at < count && k[at] < bound) ++at;
+      before += (uint32_t)at;
     }
-    __syncthreads();
+    atomicAdd(&place[tid & (kMergeElems - 1)], before);
   }
   __syncthreads();
+  if (tid < kMergeElems && e < n) out[place[tid]] = in[e];
+}
+static_assert(kPart % kMergeElems == 0, "a merge block stays within one part");
+
+// The runs of up to kSmall sorted ids, by one block.
+__global__ __launch_bounds__(kRunThreads) void small_runs_kernel(int n, int64_t table_rows, Runs r, Sums s) {
+  __shared__ uint32_t keys[kSmall];
+  __shared__ uint32_t part[17];
+  __shared__ uint32_t kept;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int items = (n + kRunThreads - 1) / kRunThreads;
+  const int first = wave * 64 * items + lane;    // item i is position first + 64 i
+  if (tid == 0) kept = (uint32_t)n;
+#pragma unroll 8
+  for (int p = tid; p < n; p += kRunThreads) keys[p] = r.pairs[p].x;
+  __syncthreads();
+  const auto load = [&](int p, uint32_t &key, bool &edge) {
+    key = p < n ? keys[p] : (uint32_t)table_rows;
+    edge = p < n && (p == 0 || keys[p - 1] != key);
+  };
   uint32_t heads = 0;
+#pragma unroll 4
   for (int i = 0; i < items; ++i) {
-    const int p = first + 64 * i;
-    const uint32_t k = p < n ? lds.key[p] : (uint32_t)table_rows;
-    const bool head = p < n && k < (uint32_t)table_rows && (p == 0 || lds.key[p - 1] != k);
-    heads += (uint32_t)__popcll(__ballot(head));
+    uint32_t key;
+    bool edge;
+    load(first + 64 * i, key, edge);
+    heads += (uint32_t)__popcll(__ballot(edge && key < (uint32_t)table_rows));
   }
   uint32_t runs;
-  uint32_t at = block_scan(lane == 0 ? heads : 0u, lds.part, runs);
+  uint32_t at = block_scan(lane == 0 ? heads : 0u, part, runs);
   at = (uint32_t)__shfl((int)at, 0, engram::kWave);
+#pragma unroll 4
   for (int i = 0; i < items; ++i) {
     const int p = first + 64 * i;
-    const uint32_t k = p < n ? lds.key[p] : (uint32_t)table_rows;
-    const bool edge = p < n && (p == 0 || lds.key[p - 1] != k);
-    const bool head = edge && k < (uint32_t)table_rows;
-    const uint64_t vote = __ballot(head);
-    const uint32_t upto = at + (uint32_t)lanes_below(vote) + (head ? 1u : 0u);
+    uint32_t key;
+    bool edge;
+    load(p, key, edge);
+    const bool valid = key < (uint32_t)table_rows;
+    const uint64_t vote = __ballot(edge && valid);
+    const uint32_t upto = at + (uint32_t)lanes_below(vote) + (edge && valid ? 1u : 0u);
     at += (uint32_t)__popcll(vote);
-    if (p < n) {
-      keys_out[p] = k;
-      order_out[p] = lds.idx[p];
-      if (head) {
-        r.starts[upto - 1] = (uint32_t)p;
-        if (s.rows != nullptr) s.rows[upto - 1] = (int64_t)k;
-      }
-      if (k < (uint32_t)table_rows && p % r.chunk == 0) r.chunk_run[p / r.chunk] = upto - 1;
-      if (edge && k == (uint32_t)table_rows) lds.kept = (uint32_t)p;
+    if (edge && valid) {
+      r.starts[upto - 1] = (uint32_t)p;
+      if (s.rows != nullptr) s.rows[upto - 1] = (int64_t)key;
     }
+    if (p < n && valid && (p & (r.chunk - 1)) == 0) r.chunk_run[p >> r.chunk_log2] = upto - 1;
+    if (edge && !valid) kept = (uint32_t)p;
   }
   __syncthreads();
   if (tid == 0) {
-    r.starts[runs] = lds.kept;
+    r.starts[runs] = kept;
     r.meta[0] = runs;
-    r.meta[1] = lds.kept;
+    r.meta[1] = kept;
     if (s.count != nullptr) s.count[0] = (int64_t)runs;
   }
 }
 
 // ---- the sort of more ids: histogram, scan, scatter per digit ---------------------
-// Block b of a pass owns a contiguous range of tiles; counts[d * blocks + b] is
+// Block b of a pass owns a contiguous range of tiles; counts[b * digits + d] is
 // how many of its keys have digit d, and after the scan how many keys with that
 // digit the blocks before it hold.
 struct Pass {
@@ -262,14 +353,14 @@ struct Pass {
 };
 
 template <bool FIRST>
-__device__ __forceinline__ uint32_t sort_key(const int64_t *ids, const uint32_t *keys, int64_t p,
-                                             int64_t table_rows) {
-  return FIRST ? key_of(ids[p], table_rows) : keys[p];
+__device__ __forceinline__ uint2 sort_pair(const int64_t *ids, const uint2 *pairs, int64_t p,
+                                           int64_t table_rows) {
+  return FIRST ? make_uint2(key_of(ids[p], table_rows), (uint32_t)p) : pairs[p];
 }
 
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(
-    const int64_t *__restrict__ ids, const uint32_t *__restrict__ keys, int64_t table_rows, Pass a,
+    const int64_t *__restrict__ ids, const uint2 *__restrict__ pairs, int64_t table_rows, Pass a,
     uint32_t *__restrict__ counts) {
   __shared__ uint32_t hist[1 << kMaxBits];
   const int digits = 1 << a.bits;
@@ -277,24 +368,42 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(
   __syncthreads();
   const int64_t p0 = blockIdx.x * a.per_block;
   const int64_t p1 = min(a.n, p0 + a.per_block);
+#pragma unroll 4
   for (int64_t p = p0 + threadIdx.x; p < p1; p += kSortThreads)
-    atomicAdd(&hist[(sort_key<FIRST>(ids, keys, p, table_rows) >> a.shift) & (digits - 1)], 1u);
+    atomicAdd(&hist[(sort_pair<FIRST>(ids, pairs, p, table_rows).x >> a.shift) & (digits - 1)], 1u);
   __syncthreads();
   for (int d = threadIdx.x; d < digits; d += kSortThreads)
-    counts[(int64_t)d * a.blocks + blockIdx.x] = hist[d];
+    counts[(int64_t)blockIdx.x * digits + d] = hist[d];
 }
 
-// One block per digit; kMaxBlocks == kSortThreads counts at most.
-__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t *__restrict__ counts,
+// A block scans kScanDigits neighbouring digits: thread (g, d) adds up its share of
+// the blocks' counts, the shares are scanned in LDS, then each count is replaced.
+__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(uint32_t *__restrict__ counts,
                                                                  uint32_t *__restrict__ totals,
-                                                                 int blocks) {
-  __shared__ uint32_t part[17];
-  uint32_t *c = counts + (int64_t)blockIdx.x * blocks;
-  const uint32_t v = (int)threadIdx.x < blocks ? c[threadIdx.x] : 0u;
-  uint32_t total;
-  const uint32_t before = block_scan(v, part, total);
-  if ((int)threadIdx.x < blocks) c[threadIdx.x] = before;
-  if (threadIdx.x == 0) totals[blockIdx.x] = total;
+                                                                 int blocks, int digits) {
+  constexpr int kShares = kScanThreads / kScanDigits;
+  __shared__ uint32_t sums[kShares][kScanDigits];
+  const int d = threadIdx.x % kScanDigits, g = threadIdx.x / kScanDigits;
+  const int digit = blockIdx.x * kScanDigits + d;
+  const bool in = digit < digits;
+  const int b0 = blocks * g / kShares, b1 = blocks * (g + 1) / kShares;
+  uint32_t sum = 0;
+  if (in) {
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) sum += counts[(int64_t)b * digits + digit];
+  }
+  sums[g][d] = sum;
+  __syncthreads();
+  uint32_t run = 0;
+  for (int q = 0; q < g; ++q) run += sums[q][d];
+  if (!in) return;
+  if (g == kShares - 1) totals[digit] = run + sum;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const uint32_t c = counts[(int64_t)b * digits + digit];
+    counts[(int64_t)b * digits + digit] = run;
+    run += c;
+  }
 }
 
 struct ScatterLds {
@@ -305,10 +414,9 @@ struct ScatterLds {
 
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
-    const int64_t *__restrict__ ids, const uint32_t *__restrict__ keys,
-    const uint32_t *__restrict__ order, int64_t table_rows, Pass a,
+    const int64_t *__restrict__ ids, const uint2 *__restrict__ pairs, int64_t table_rows, Pass a,
     const uint32_t *__restrict__ counts, const uint32_t *__restrict__ totals,
-    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ order_out) {
+    uint2 *__restrict__ out) {
   __shared__ ScatterLds lds;
   constexpr int kWaves = kSortThreads / 64;
   constexpr int kPer = (1 << kMaxBits) / kSortThreads;     // digits of a thread
@@ -326,7 +434,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int d = tid * kPer + k;
-      if (d < digits) lds.base[d] = before + counts[(int64_t)d * a.blocks + blockIdx.x];
+      if (d < digits) lds.base[d] = before + counts[(int64_t)blockIdx.x * digits + d];
       before += t[k];
     }
   }
@@ -335,24 +443,17 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
   for (int64_t tile = p0; tile < p1; tile += kSortTile) {
     for (int d = lane; d < digits; d += 64) lds.cnt[wave][d] = 0u;
     const int64_t first = tile + wave * 64 * kSortItems + lane;
-    uint32_t key[kSortItems], idx[kSortItems], rank[kSortItems];
+    uint2 pair[kSortItems];
+    uint32_t rank[kSortItems];
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
       const int64_t p = first + 64 * i;
-      key[i] = p < p1 ? sort_key<FIRST>(ids, keys, p, table_rows) : 0u;
-      idx[i] = FIRST ? (uint32_t)p : p < p1 ? order[p] : 0u;
+      pair[i] = p < p1 ? sort_pair<FIRST>(ids, pairs, p, table_rows) : make_uint2(0u, 0u);
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kSortItems; ++i) {
-      const bool in = first + 64 * i < p1;
-      const uint32_t d = (key[i] >> a.shift) & (uint32_t)(digits - 1);
-      const uint64_t mask = same_digit<kMaxBits>(d, a.bits) & __ballot(in);
-      uint32_t before = 0;
-      const int leader = mask ? __ffsll((unsigned long long)mask) - 1 : 0;
-      if (in && lane == leader) before = atomicAdd(&lds.cnt[wave][d], (uint32_t)__popcll(mask));
-      rank[i] = (uint32_t)__shfl((int)before, leader, engram::kWave) + (uint32_t)lanes_below(mask);
-    }
+    wave_ranks<kMaxBits, kSortItems>(
+        lds.cnt[wave], a.bits, [&](int i) { return (pair[i].x >> a.shift) & (uint32_t)(digits - 1); },
+        [&](int i) { return first + 64 * i < p1; }, rank);
     __syncthreads();
     for (int d = tid; d < digits; d += kSortThreads) {
       uint32_t run = lds.base[d];
@@ -368,63 +469,77 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
 #pragma unroll
     for (int i = 0; i < kSortItems; ++i) {
       if (first + 64 * i < p1) {
-        const uint32_t d = (key[i] >> a.shift) & (uint32_t)(digits - 1);
-        const uint32_t to = lds.cnt[wave][d] + rank[i];
-        keys_out[to] = key[i];
-        order_out[to] = idx[i];
+        const uint32_t d = (pair[i].x >> a.shift) & (uint32_t)(digits - 1);
+        out[lds.cnt[wave][d] + rank[i]] = pair[i];
       }
     }
     __syncthreads();
   }
 }
 
-// Runs of the sorted keys: the heads of each tile, then their numbers.
-__device__ __forceinline__ bool is_edge(const uint32_t *keys, int64_t p, uint32_t k) {
-  return p == 0 || keys[p - 1] != k;
+// Runs of the sorted keys: the heads of each tile, then their numbers. Item i of a
+// thread is position first + 64 i, so a wave's positions are contiguous.
+constexpr int kHeadThreads = 512;
+constexpr int kHeadItems = 8;
+constexpr int kHeadTile = kHeadThreads * kHeadItems;
+
+__device__ __forceinline__ void load_heads(const uint2 *pairs, int64_t n, int64_t first, uint32_t none,
+                                           uint32_t (&key)[kHeadItems], uint32_t (&before)[kHeadItems]) {
+#pragma unroll
+  for (int i = 0; i < kHeadItems; ++i) {
+    const int64_t p = first + 64 * i;
+    key[i] = p < n ? pairs[p].x : none;
+    before[i] = p > 0 && p < n ? pairs[p - 1].x : ~key[i];
+  }
 }
 
-__global__ __launch_bounds__(kSortThreads) void count_heads_kernel(
-    const uint32_t *__restrict__ keys, int64_t n, int64_t table_rows,
-    uint32_t *__restrict__ tile_heads) {
+__global__ __launch_bounds__(kHeadThreads) void count_heads_kernel(
+    const uint2 *__restrict__ pairs, int64_t n, int64_t table_rows, uint32_t *__restrict__ tile_heads) {
   __shared__ uint32_t part[17];
-  const int64_t tile = (int64_t)blockIdx.x * kSortTile;
-  uint32_t heads = 0, total;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t key[kHeadItems], before[kHeadItems], heads = 0, total;
+  load_heads(pairs, n, (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane,
+             (uint32_t)table_rows, key, before);
 #pragma unroll
-  for (int i = 0; i < kSortItems; ++i) {
-    const int64_t p = tile + i * kSortThreads + threadIdx.x;
-    if (p < n) {
-      const uint32_t k = keys[p];
-      heads += k < (uint32_t)table_rows && is_edge(keys, p, k) ? 1u : 0u;
-    }
-  }
+  for (int i = 0; i < kHeadItems; ++i)
+    heads += key[i] < (uint32_t)table_rows && before[i] != key[i] ? 1u : 0u;
   block_scan(heads, part, total);
   if (threadIdx.x == 0) tile_heads[blockIdx.x] = total;
 }
 
-__global__ __launch_bounds__(kSortThreads) void write_runs_kernel(
+__global__ __launch_bounds__(kHeadThreads) void write_runs_kernel(
     int64_t n, int64_t table_rows, const uint32_t *__restrict__ tile_heads, Runs r, Sums s) {
   __shared__ uint32_t part[17];
-  uint32_t v = 0, at;
-  for (int64_t t = threadIdx.x; t < (int64_t)blockIdx.x; t += kSortThreads) v += tile_heads[t];
-  block_scan(v, part, at);                      // runs that begin before this tile
-  const int64_t tile = (int64_t)blockIdx.x * kSortTile;
-  for (int i = 0; i < kSortItems; ++i) {
-    const int64_t p = tile + i * kSortThreads + threadIdx.x;
-    const uint32_t k = p < n ? r.keys[p] : (uint32_t)table_rows;
-    const bool edge = p < n && is_edge(r.keys, p, k);
-    const bool head = edge && k < (uint32_t)table_rows;
-    uint32_t total;
-    const uint32_t upto = at + block_scan(head ? 1u : 0u, part, total) + (head ? 1u : 0u);
-    at += total;
-    if (p >= n) continue;                       // no barrier follows in this iteration
-    if (head) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t first = (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane;
+  uint32_t key[kHeadItems], before[kHeadItems];
+  load_heads(r.pairs, n, first, (uint32_t)table_rows, key, before);
+  uint32_t v = 0, tiles_before, total;
+  for (int64_t t = threadIdx.x; t < (int64_t)blockIdx.x; t += kHeadThreads) v += tile_heads[t];
+  block_scan(v, part, tiles_before);             // runs that begin before this tile
+  uint32_t heads = 0;
+#pragma unroll
+  for (int i = 0; i < kHeadItems; ++i)
+    heads += (uint32_t)__popcll(__ballot(key[i] < (uint32_t)table_rows && before[i] != key[i]));
+  uint32_t at = block_scan(lane == 0 ? heads : 0u, part, total);
+  at = tiles_before + (uint32_t)__shfl((int)at, 0, engram::kWave);
+#pragma unroll
+  for (int i = 0; i < kHeadItems; ++i) {
+    const int64_t p = first + 64 * i;
+    const bool in = p < n;
+    const bool edge = in && before[i] != key[i];
+    const bool valid = key[i] < (uint32_t)table_rows;
+    const uint64_t vote = __ballot(edge && valid);
+    const uint32_t upto = at + (uint32_t)lanes_below(vote) + (edge && valid ? 1u : 0u);
+    at += (uint32_t)__popcll(vote);
+    if (edge && valid) {
       r.starts[upto - 1] = (uint32_t)p;
-      if (s.rows != nullptr) s.rows[upto - 1] = (int64_t)k;
+      if (s.rows != nullptr) s.rows[upto - 1] = (int64_t)key[i];
     }
-    if (k < (uint32_t)table_rows && p % r.chunk == 0) r.chunk_run[p / r.chunk] = upto - 1;
+    if (in && valid && (p & (r.chunk - 1)) == 0) r.chunk_run[p >> r.chunk_log2] = upto - 1;
     // the end of the kept ids: the first dropped one, or behind the last position
-    const bool dropped = edge && k == (uint32_t)table_rows;
-    if (dropped || (p == n - 1 && k < (uint32_t)table_rows)) {
+    const bool dropped = edge && !valid;
+    if (dropped || (p == n - 1 && valid)) {
       const uint32_t kept = (uint32_t)(dropped ? p : n);
       r.starts[upto] = kept;
       r.meta[0] = upto;
@@ -451,7 +566,7 @@ __device__ __forceinline__ LastRun last_run(const Runs &r, uint32_t c, uint32_t 
   }
   l.start = r.starts[l.run];
   l.end = r.starts[l.run + 1];
-  l.is_long = l.start >= p0 && l.end - l.start > (uint32_t)kLong;
+  l.is_long = l.start >= p0 && l.end - l.start > (uint32_t)r.longest;
   return l;
 }
 
@@ -515,7 +630,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(
   if (s0 < p0) {                      // a run from an earlier chunk leads
     const uint32_t e0 = r.starts[u + 1];
     const uint32_t pe = min(e0, p1);
-    if (e0 - s0 > (uint32_t)kLong) {
+    if (e0 - s0 > (uint32_t)r.longest) {
       float acc[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
@@ -523,7 +638,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(
         Cols<F32, VEC> v[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
-          v[j].load(d_out, (int64_t)r.order[min(p + j, pe - 1)] * out_ld + col);
+          v[j].load(d_out, (int64_t)r.pairs[min(p + j, pe - 1)].y * out_ld + col);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           if (p + j < pe) {
@@ -544,26 +659,25 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
   for (; p < end; p += kAhead) {
-    uint32_t k[kAhead + 1];
+    uint2 k[kAhead + 1];
     Cols<F32, VEC> v[kAhead];
 #pragma unroll
-    for (int j = 0; j <= kAhead; ++j) k[j] = r.keys[min(p + j, end - 1)];
+    for (int j = 0; j <= kAhead; ++j) k[j] = r.pairs[min(p + j, end - 1)];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      v[j].load(d_out, (int64_t)r.order[min(p + j, end - 1)] * out_ld + col);
+    for (int j = 0; j < kAhead; ++j) v[j].load(d_out, (int64_t)k[j].y * out_ld + col);
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (p + j >= end) continue;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] += v[j][e];
       const bool last = p + j == end - 1;
-      if (last || k[j + 1] != k[j]) {
+      if (last || k[j + 1].x != k[j].x) {
         if (last && l.is_long) {
           put<VEC>(pieces + (int64_t)(2 * (uint64_t)c + 1) * piece_ld + col, acc, false);
         } else {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) acc[e] *= scale;
-          put<VEC>(s.grad + (int64_t)(s.dense ? k[j] : u) * s.ld + col, acc, s.accumulate);
+          put<VEC>(s.grad + (int64_t)(s.dense ? k[j].x : u) * s.ld + col, acc, s.accumulate);
         }
         ++u;
 #pragma unroll
@@ -573,16 +687,44 @@ __global__ __launch_bounds__(kSumThreads) void sum_runs_kernel(
   }
 }
 
-// The long runs: block b joins the pieces of those that begin in its
-// kJoinChunks chunks. The threads form groups of one thread per column (4 columns
-// where VEC is 4); group g adds a fixed share of the pieces in order, and the
-// first group adds the groups in order. Also closes the list of rows with -1.
+// The pieces [k0, k1) of the long run that begins in chunk c, added in order.
+template <int VEC>
+__device__ __forceinline__ void add_pieces(const float *__restrict__ pieces, int64_t piece_ld, int64_t col,
+                                           int64_t c, int64_t k0, int64_t k1, float (&acc)[VEC]) {
+  for (int64_t k = k0; k < k1; k += kAhead) {
+    float v[kAhead][VEC];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t kk = k + j < k1 ? k + j : k1 - 1;
+      const float *q = pieces + (kk == 0 ? 2 * c + 1 : 2 * (c + kk)) * piece_ld + col;
+      if (VEC == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(q);
+        v[j][0] = x.x; v[j][1 % VEC] = x.y; v[j][2 % VEC] = x.z; v[j][3 % VEC] = x.w;
+      } else {
+        v[j][0] = *q;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k + j < k1) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += v[j][e];
+      }
+    }
+  }
+}
+
+// The long runs: block b joins the pieces of those that begin in its kJoinChunks
+// chunks. The threads form groups of one thread per column (4 columns where VEC is
+// 4). A run of few pieces is one group's, added in order; of a longer one each group
+// adds a fixed share of the pieces in order, and the first group adds the groups
+// in order. Also closes the list of rows with -1.
 template <int VEC>
 __global__ __launch_bounds__(kJoinThreads) void join_pieces_kernel(
     Runs r, Sums s, const float *__restrict__ pieces, int64_t piece_ld, int cols, int width,
     int64_t chunks, int64_t n, float scale) {
   __shared__ float sums[kJoinThreads * VEC];
-  __shared__ uint32_t list[kJoinChunks];
+  __shared__ LastRun list[kJoinChunks];
   const int tid = threadIdx.x;
   const uint32_t runs = r.meta[0], kept = r.meta[1];
   const int64_t c0 = (int64_t)blockIdx.x * kJoinChunks;
@@ -591,54 +733,50 @@ __global__ __launch_bounds__(kJoinThreads) void join_pieces_kernel(
     for (int64_t u = c0 * r.chunk + tid; u < last; u += kJoinThreads)
       if (u >= (int64_t)runs) s.rows[u] = -1;
   }
+  bool any = false;
   if (tid < kJoinChunks) {
     const int64_t c = c0 + tid;
-    uint32_t found = 0;
+    LastRun l;
+    l.is_long = false;
     if (c < chunks && c * r.chunk < (int64_t)kept) {
       const uint32_t p0 = (uint32_t)c * (uint32_t)r.chunk;
-      found = last_run(r, (uint32_t)c, p0, min(p0 + (uint32_t)r.chunk, kept), runs, kept).is_long;
+      l = last_run(r, (uint32_t)c, p0, min(p0 + (uint32_t)r.chunk, kept), runs, kept);
     }
-    list[tid] = found;
+    list[tid] = l;
+    any = l.is_long;
   }
-  __syncthreads();
+  if (!__syncthreads_or(any)) return;
   const int groups = kJoinThreads / width;
   const int group = tid / width;
   const int g = blockIdx.y * width + (tid - group * width);
   const bool active = group < groups && g < cols;
+  const int64_t col = (int64_t)g * VEC;
+  const auto count = [&](int t) {
+    return (int64_t)((list[t].end - 1) >> r.chunk_log2) - (c0 + t) + 1;
+  };
+  const auto store = [&](const LastRun &l, const float (&acc)[VEC]) {
+    float *dst = s.grad + (int64_t)(s.dense ? r.pairs[l.start].x : l.run) * s.ld + col;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) dst[e] = s.accumulate ? dst[e] + acc[e] * scale : acc[e] * scale;
+  };
+  if (active) {
+    for (int t = group; t < kJoinChunks; t += groups) {
+      if (!list[t].is_long || count(t) > kFewPieces) continue;
+      float acc[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+      add_pieces<VEC>(pieces, piece_ld, col, c0 + t, 0, count(t), acc);
+      store(list[t], acc);
+    }
+  }
   for (int t = 0; t < kJoinChunks; ++t) {
-    if (!list[t]) continue;                     // the same for the whole block
-    const uint32_t c = (uint32_t)(c0 + t);
-    const uint32_t p0 = c * (uint32_t)r.chunk;
-    const LastRun l = last_run(r, c, p0, min(p0 + (uint32_t)r.chunk, kept), runs, kept);
-    const int64_t m = (int64_t)((l.end - 1) / (uint32_t)r.chunk) - c + 1;
+    if (!list[t].is_long || count(t) <= kFewPieces) continue;      // the same for the whole block
+    const int64_t m = count(t);
     float acc[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-    if (active) {
-      const int64_t k1 = m * (group + 1) / groups;
-      for (int64_t k = m * group / groups; k < k1; k += kAhead) {
-        float v[kAhead][VEC];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const int64_t kk = k + j < k1 ? k + j : k1 - 1;
-          const float *q = pieces + (kk == 0 ? 2 * (int64_t)c + 1 : 2 * ((int64_t)c + kk)) * piece_ld +
-                           (int64_t)g * VEC;
-          if (VEC == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(q);
-            v[j][0] = x.x; v[j][1 % VEC] = x.y; v[j][2 % VEC] = x.z; v[j][3 % VEC] = x.w;
-          } else {
-            v[j][0] = *q;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (k + j < k1) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += v[j][e];
-          }
-        }
-      }
-    }
+    if (active)
+      add_pieces<VEC>(pieces, piece_ld, col, c0 + t, m * group / groups, m * (group + 1) / groups, acc);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sums[e * kJoinThreads + tid] = acc[e];
     __syncthreads();
@@ -647,10 +785,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_pieces_kernel(
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] += sums[e * kJoinThreads + q * width + tid];
       }
-      float *dst = s.grad + (int64_t)(s.dense ? r.keys[l.start] : l.run) * s.ld + (int64_t)g * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        dst[e] = s.accumulate ? dst[e] + acc[e] * scale : acc[e] * scale;
+      store(list[t], acc);
     }
     __syncthreads();
   }
@@ -660,33 +795,36 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // The workspace of a call, and how it is cut.
 struct Plan {
-  int64_t n, chunks, tiles;
-  int chunk, bits, passes, digit;
+  int64_t n, chunks, head_tiles;
+  int chunk, longest, bits, passes, digit;
   bool vec;
   int64_t piece_ld;
-  size_t keys[2], order[2], counts, totals, tile_heads, starts, chunk_run, meta, pieces, bytes;
+  size_t pairs[2], counts, totals, tile_heads, starts, chunk_run, meta, pieces, bytes;
   Pass pass;
 };
 
-// Chunks of 64 positions where those give every CU 2048 threads, else shorter
-// ones down to 8, so that small calls use the chip.
+// Chunks of 64 positions where those give every CU 2048 threads, else shorter ones
+// down to 8, so that small calls use the chip; a thread follows a run behind its
+// chunk for as long as a chunk, up to 64 positions in all.
 Plan make_plan(const EngramEmbedArgs &a) {
   Plan p;
   p.n = a.n_ids;
   p.vec = a.dim % 8 == 0 && a.out_ld % 8 == 0 && a.grad_ld % 4 == 0;
   const int64_t per_chunk = p.vec ? a.dim / 8 : a.dim;
-  p.chunk = kLong;
+  p.chunk = kMaxChunk;
   while (p.chunk > 8 && (p.n / p.chunk) * per_chunk < (int64_t)256 * 2048) p.chunk /= 2;
+  p.longest = 2 * p.chunk < kMaxChunk ? 2 * p.chunk : kMaxChunk;
   p.chunks = (p.n + p.chunk - 1) / p.chunk;
   p.bits = 1;
   while (p.bits < 32 && (a.table_rows >> p.bits) != 0) ++p.bits;
   p.passes = (p.bits + kMaxBits - 1) / kMaxBits;
   p.digit = (p.bits + p.passes - 1) / p.passes;
-  p.tiles = (p.n + kSortTile - 1) / kSortTile;
-  const int64_t per = p.tiles > 0 ? (p.tiles + kMaxBlocks - 1) / kMaxBlocks : 1;
+  p.head_tiles = (p.n + kHeadTile - 1) / kHeadTile;
+  const int64_t tiles = (p.n + kSortTile - 1) / kSortTile;
+  const int64_t per = tiles > 0 ? (tiles + kMaxBlocks - 1) / kMaxBlocks : 1;
   p.pass.n = p.n;
   p.pass.per_block = per * kSortTile;
-  p.pass.blocks = (int)((p.tiles + per - 1) / per);
+  p.pass.blocks = (int)((tiles + per - 1) / per);
   p.piece_ld = ((int64_t)a.dim + 3) / 4 * 4;
   const bool large = p.n > kSmall;
   size_t at = 0;
@@ -695,13 +833,10 @@ Plan make_plan(const EngramEmbedArgs &a) {
     at += align256(bytes);
     return here;
   };
-  for (int i = 0; i < 2; ++i) {
-    p.keys[i] = i == 0 || large ? take((size_t)p.n * 4) : 0;
-    p.order[i] = i == 0 || large ? take((size_t)p.n * 4) : 0;
-  }
+  for (int i = 0; i < 2; ++i) p.pairs[i] = take((size_t)p.n * 8);
   p.counts = take(large ? ((size_t)p.pass.blocks << p.digit) * 4 : 0);
   p.totals = take(large ? (size_t)4 << p.digit : 0);
-  p.tile_heads = take(large ? (size_t)p.tiles * 4 : 0);
+  p.tile_heads = take(large ? (size_t)p.head_tiles * 4 : 0);
   p.starts = take((size_t)(p.n + 1) * 4);
   p.chunk_run = take((size_t)p.chunks * 4);
   p.meta = take(8);
@@ -726,7 +861,7 @@ template <int VEC>
 void launch_join(const EngramEmbedArgs &a, const Plan &p, const Runs &r, const Sums &s,
                  const float *pieces, hipStream_t stream) {
   const int cols = VEC == 4 ? a.dim / 4 : a.dim;
-  const int slices = (cols + 255) / 256;
+  const int slices = (cols + 63) / 64;
   const int width = (cols + slices - 1) / slices;
   const dim3 grid((unsigned)((p.chunks + kJoinChunks - 1) / kJoinChunks), (unsigned)slices);
   hipLaunchKernelGGL((join_pieces_kernel<VEC>), grid, dim3(kJoinThreads), 0, stream, r, s, pieces,
@@ -743,59 +878,62 @@ hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
                                     hipStream_t stream) {
   const Plan p = make_plan(a);
   uint8_t *ws = (uint8_t *)workspace;
-  uint32_t *keys[2] = {(uint32_t *)(ws + p.keys[0]), (uint32_t *)(ws + p.keys[1])};
-  uint32_t *order[2] = {(uint32_t *)(ws + p.order[0]), (uint32_t *)(ws + p.order[1])};
+  uint2 *pairs[2] = {(uint2 *)(ws + p.pairs[0]), (uint2 *)(ws + p.pairs[1])};
   uint32_t *counts = (uint32_t *)(ws + p.counts), *totals = (uint32_t *)(ws + p.totals);
   uint32_t *tile_heads = (uint32_t *)(ws + p.tile_heads);
   float *pieces = (float *)(ws + p.pieces);
   const bool dense = n_rows == nullptr;
   const Sums s{grad, a.grad_ld, grad_rows, n_rows, dense ? 1 : 0, accumulate};
-  const int zero_vec = a.dim % 4 == 0 && a.grad_ld % 4 == 0 ? 1 : 0;
-  const EngramFastDiv zero_groups(zero_vec ? a.dim / 4 : a.dim);
-  const int64_t zero_total = dense && !accumulate ? a.table_rows * zero_groups.d : 0;
-  Runs r{keys[0], order[0], (uint32_t *)(ws + p.starts), (uint32_t *)(ws + p.chunk_run),
-         (uint32_t *)(ws + p.meta), p.chunk};
+  const bool zero_vec = a.dim % 4 == 0 && a.grad_ld % 4 == 0;
+  Zero z{EngramFastDiv(zero_vec ? a.dim / 4 : a.dim), 0, zero_vec, zero_vec && a.grad_ld == a.dim};
+  if (dense && !accumulate) z.total = a.table_rows * z.groups.d;
+  // clearing: 8192 blocks of 256 threads at most
+  const int64_t zero_want = (z.total + 256 * 4 - 1) / (256 * 4);
+  const unsigned zero_blocks = (unsigned)(zero_want < 8192 ? zero_want : 8192);
+  Runs r{pairs[1], (uint32_t *)(ws + p.starts), (uint32_t *)(ws + p.chunk_run),
+         (uint32_t *)(ws + p.meta), p.chunk, __builtin_ctz(p.chunk), p.longest};
   if (p.n <= kSmall) {
-    const int64_t want = (zero_total + (int64_t)kSmallThreads * 4 - 1) / (kSmallThreads * 4);
-    const unsigned blocks = 1u + (unsigned)(want < 1024 ? want : 1024);
-    hipLaunchKernelGGL(small_sort_kernel, dim3(blocks), dim3(kSmallThreads), 0, stream, row_ids,
-                       (int)p.n, a.table_rows, p.bits, r, keys[0], order[0], s, zero_groups,
-                       zero_vec, zero_total);
+    const int parts = (int)((p.n + kPart - 1) / kPart);
+    uint2 *sorted = pairs[parts > 1 ? 0 : 1];
+    if (parts + zero_blocks > 0)
+      hipLaunchKernelGGL(sort_part_kernel, dim3((unsigned)parts + zero_blocks), dim3(kPartThreads), 0,
+                         stream, row_ids, (int)p.n, a.table_rows, p.bits, sorted, parts, s, z);
+    if (parts > 1)
+      hipLaunchKernelGGL(merge_parts_kernel,
+                         dim3((unsigned)((p.n + kMergeElems - 1) / kMergeElems)), dim3(kMergeThreads), 0,
+                         stream, (const uint2 *)sorted, (int)p.n, pairs[1]);
+    hipLaunchKernelGGL(small_runs_kernel, dim3(1), dim3(kRunThreads), 0, stream, (int)p.n, a.table_rows,
+                       r, s);
   } else {
-    if (zero_total > 0) {
-      const int64_t want = (zero_total + 256 * 4 - 1) / (256 * 4);
-      hipLaunchKernelGGL(zero_grad_kernel, dim3((unsigned)(want < 8192 ? want : 8192)), dim3(256), 0,
-                         stream, s, zero_groups, zero_vec, zero_total);
-    }
+    if (zero_blocks > 0)
+      hipLaunchKernelGGL(zero_grad_kernel, dim3(zero_blocks), dim3(256), 0, stream, s, z);
     Pass pass = p.pass;
-    int at = 1;                       // the buffers the next pass writes are 1 - at
+    int at = 1;                       // the next pass writes pairs[1 - at]
     for (int i = 0; i < p.passes; ++i) {
       pass.shift = i * p.digit;
       pass.bits = p.digit;
       const dim3 grid((unsigned)pass.blocks), block(kSortThreads);
+      const uint2 *from = pairs[at];
       if (i == 0)
-        hipLaunchKernelGGL(sort_count_kernel<true>, grid, block, 0, stream, row_ids,
-                           (const uint32_t *)nullptr, a.table_rows, pass, counts);
+        hipLaunchKernelGGL(sort_count_kernel<true>, grid, block, 0, stream, row_ids, from, a.table_rows,
+                           pass, counts);
       else
-        hipLaunchKernelGGL(sort_count_kernel<false>, grid, block, 0, stream, row_ids,
-                           (const uint32_t *)keys[at], a.table_rows, pass, counts);
-      hipLaunchKernelGGL(sort_scan_kernel, dim3(1u << p.digit), block, 0, stream, counts, totals,
-                         pass.blocks);
+        hipLaunchKernelGGL(sort_count_kernel<false>, grid, block, 0, stream, row_ids, from, a.table_rows,
+                           pass, counts);
+      hipLaunchKernelGGL(sort_scan_kernel, dim3(((1u << p.digit) + kScanDigits - 1) / kScanDigits),
+                         dim3(kScanThreads), 0, stream, counts, totals, pass.blocks, 1 << p.digit);
       if (i == 0)
-        hipLaunchKernelGGL(sort_scatter_kernel<true>, grid, block, 0, stream, row_ids,
-                           (const uint32_t *)nullptr, (const uint32_t *)nullptr, a.table_rows, pass,
-                           counts, totals, keys[1 - at], order[1 - at]);
+        hipLaunchKernelGGL(sort_scatter_kernel<true>, grid, block, 0, stream, row_ids, from, a.table_rows,
+                           pass, counts, totals, pairs[1 - at]);
       else
-        hipLaunchKernelGGL(sort_scatter_kernel<false>, grid, block, 0, stream, row_ids,
-                           (const uint32_t *)keys[at], (const uint32_t *)order[at], a.table_rows,
-                           pass, counts, totals, keys[1 - at], order[1 - at]);
+        hipLaunchKernelGGL(sort_scatter_kernel<false>, grid, block, 0, stream, row_ids, from, a.table_rows,
+                           pass, counts, totals, pairs[1 - at]);
       at = 1 - at;
     }
-    r.keys = keys[at];
-    r.order = order[at];
-    hipLaunchKernelGGL(count_heads_kernel, dim3((unsigned)p.tiles), dim3(kSortThreads), 0, stream,
-                       r.keys, p.n, a.table_rows, tile_heads);
-    hipLaunchKernelGGL(write_runs_kernel, dim3((unsigned)p.tiles), dim3(kSortThreads), 0, stream,
+    r.pairs = pairs[at];
+    hipLaunchKernelGGL(count_heads_kernel, dim3((unsigned)p.head_tiles), dim3(kHeadThreads), 0, stream,
+                       r.pairs, p.n, a.table_rows, tile_heads);
+    hipLaunchKernelGGL(write_runs_kernel, dim3((unsigned)p.head_tiles), dim3(kHeadThreads), 0, stream,
                        p.n, a.table_rows, tile_heads, r, s);
   }
   hipError_t err = hipGetLastError();

@@ -141,8 +141,8 @@ def _check_sparse(ids, d_out, R, dim, ot, scale, out_ld=0):
     return rows, grad
 
 
-# (n, rows of the table, dim, ids): sizes on both sides of the one-block sort's
-# 16384 ids and of a sort tile's 4096, runs on both sides of 64
+# (n, rows of the table, dim, ids): sizes around the parts of 1024 ids, the merge's
+# limit of 32768 and the large sort's tiles, runs on both sides of 64
 SPREAD = [
     (1, 5, 8, "uniform"), (2, 1, 3, "uniform"), (63, 7, 256, "uniform"), (64, 1, 8, "uniform"),
     (65, 1, 8, "uniform"), (129, 2, 40, "uniform"), (1000, 100_000, 256, "uniform"),
@@ -150,6 +150,8 @@ SPREAD = [
     (16384, 100, 16, "zipf"), (16385, 100, 16, "zipf"), (16385, 50_000, 72, "uniform"),
     (20481, 384_006_168, 64, "uniform"), (40_000, 4_294_967_294, 8, "uniform"),
     (100_003, 1000, 24, "zipf"), (100_003, 1, 8, "uniform"), (300_000, 2_000_000, 8, "zipf"),
+    (1024, 700, 16, "zipf"), (1025, 4_294_967_294, 16, "uniform"), (2048, 1, 16, "uniform"),
+    (32768, 5000, 16, "zipf"), (32769, 5000, 16, "zipf"), (33_000, 3, 40, "zipf"),
     (30_000, 9, 7, "zipf"), (3000, 50, 5120, "zipf"), (500, 20, 2056, "zipf"), (400, 11, 1030, "zipf"),
     (2_200_000, 700_000, 4, "zipf")]
 
@@ -182,7 +184,7 @@ def test_grad_run_lengths(lengths):
     _check_sparse(ids, _rand((ids.numel(), 40), 9, torch.float32), 3 * len(lengths), 40, E.F32, 1.0)
 
 
-@pytest.mark.parametrize("n", [0, 1, 500, 16384, 16385, 50_000])
+@pytest.mark.parametrize("n", [0, 1, 500, 16384, 32768, 32769, 50_000])
 def test_grad_no_id_in_the_table(n):
     say("grad: nothing kept", n)
     ids = torch.full((n,), -1, dtype=torch.int64)
@@ -199,7 +201,7 @@ def test_grad_no_id_in_the_table(n):
 @pytest.mark.parametrize("ot", [E.BF16, E.F32])
 @pytest.mark.parametrize("n,R,dim,out_ld,table_ld", [
     (300, 50, 24, 0, 0), (300, 50, 24, 32, 28), (5000, 2000, 13, 17, 15), (20_000, 999, 64, 0, 0),
-    (17_000, 3, 8, 8, 16), (40, 100_000, 256, 264, 256), (700, 30, 1032, 0, 1036)])
+    (37_000, 3, 8, 8, 16), (40, 100_000, 256, 264, 256), (700, 30, 1032, 0, 1036)])
 def test_grad_dense_written_and_added(ot, n, R, dim, out_ld, table_ld):
     say("grad dense", ot, n, R, dim, out_ld, table_ld)
     ids = _ids(n, R, "zipf", n)
@@ -260,7 +262,7 @@ def test_grad_is_the_lookup_s_adjoint_and_difference():
     assert abs(left - right) <= (tol.sum(0).max() * dim * 4).item() + 1e-9 * abs(left)
 
 
-@pytest.mark.parametrize("n,R", [(3000, 40), (30_000, 40), (30_000, 1_000_000)])
+@pytest.mark.parametrize("n,R", [(900, 30), (3000, 40), (40_000, 40), (40_000, 1_000_000)])
 def test_grad_same_bits_twice_and_in_a_graph(n, R):
     say("grad: repeat and replay", n, R)
     dim = 64
