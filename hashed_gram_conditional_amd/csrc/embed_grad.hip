@@ -4,11 +4,12 @@
 //
 //   1. Keys: the row id, or table_rows for an id outside the table (those sort
 //      behind every row and are dropped). A stable sort of (key, i) puts each
-//      row's occurrences side by side in the order of i. Up to kSmall ids blocks
-//      of kPart are sorted in LDS and merged by rank: an element's place is its
-//      place in its own part plus, for every other part, a binary search. Above,
-//      a least-digit radix sort: each pass is a histogram per block, a scan per
-//      digit and a scatter.
+//      row's occurrences side by side in the order of i. Up to kSmall ids, parts
+//      of kPart are sorted by counting and merged by rank: an element's place is
+//      its place in its own part plus, for every other part, a binary search.
+//      Above, a least-digit radix sort: each pass is a histogram per block, a scan
+//      per digit and a scatter. (Three launches of about 5 us against nine of 5 to
+//      18 us; at 32768 ids the merge's searches still cost less.)
 //   2. Runs of equal keys: run u starts at sorted position starts[u]; the number
 //      of runs is known only on the device.
 //   3. Sums: the sorted positions are cut into chunks of `chunk`; a thread owns
@@ -26,10 +27,7 @@
 
 namespace {
 
-constexpr int kPart = 1024;            // ids a block sorts in LDS
-constexpr int kPartThreads = 256;
-constexpr int kPartItems = kPart / kPartThreads;
-constexpr int kPartBits = 8;
+constexpr int kPart = 256;             // ids a block sorts, one per thread
 constexpr int kSmall = 32768;          // ids whose keys one block holds in LDS to merge
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeElems = 64;
@@ -42,7 +40,6 @@ constexpr int kMaxBits = 11;           // digit of one pass of the large sort
 constexpr int kMaxBlocks = 1024;       // blocks of one pass
 constexpr int kScanThreads = 1024;
 constexpr int kScanDigits = 32;
-constexpr int kRunThreads = 1024;
 
 constexpr int kSumThreads = 256;
 constexpr int kJoinThreads = 512;
@@ -151,7 +148,7 @@ struct Sums {
 // or single columns.
 struct Zero {
   EngramFastDiv groups;
-  int64_t total;              // groups in all; 0: nothing to do
+  int64_t begin, end;         // groups to clear
   int vec, flat;
 };
 
@@ -159,10 +156,11 @@ __device__ __forceinline__ void zero_grad(const Sums &s, const Zero &z, int64_t 
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
   if (z.flat) {
 #pragma unroll 4
-    for (int64_t g = first; g < z.total; g += step) reinterpret_cast<float4 *>(s.grad)[g] = none;
+    for (int64_t g = z.begin + first; g < z.end; g += step)
+      reinterpret_cast<float4 *>(s.grad)[g] = none;
     return;
   }
-  for (int64_t g = first; g < z.total; g += step) {
+  for (int64_t g = z.begin + first; g < z.end; g += step) {
     const int64_t row = z.groups.div(g);
     const int64_t col = g - row * z.groups.d;
     if (z.vec)
@@ -177,87 +175,59 @@ __global__ __launch_bounds__(256) void zero_grad_kernel(Sums s, Zero z) {
 }
 
 // ---- the sort of up to kSmall ids -------------------------------------------------
-// Block b < parts: a stable radix sort of part b. The other blocks (a dense gradient
-// that is not added to) clear the gradient meanwhile.
-__global__ __launch_bounds__(kPartThreads) void sort_part_kernel(
-    const int64_t *__restrict__ ids, int n, int64_t table_rows, int bits, uint2 *__restrict__ out,
-    int parts, Sums s, Zero z) {
-  constexpr int kWaves = kPartThreads / 64;
-  __shared__ uint32_t keys[kPart];
-  __shared__ uint16_t order[kPart];
-  __shared__ uint32_t cnt[kWaves][1 << kPartBits];
-  __shared__ uint32_t part[17];
-  if ((int)blockIdx.x >= parts) {
-    zero_grad(s, z, (int64_t)(blockIdx.x - parts) * kPartThreads + threadIdx.x,
-              (int64_t)(gridDim.x - parts) * kPartThreads);
-    return;
-  }
+// The first blocks of a launch do its work; the others (a dense gradient that is not
+// added to) clear their share of the gradient meanwhile.
+template <int THREADS>
+__device__ __forceinline__ bool zero_block(const Sums &s, const Zero &z, int blocks) {
+  if ((int)blockIdx.x < blocks) return false;
+  zero_grad(s, z, (int64_t)(blockIdx.x - blocks) * THREADS + threadIdx.x,
+            (int64_t)(gridDim.x - blocks) * THREADS);
+  return true;
+}
+
+// Block b: part b in order. A thread counts the part's keys that come before its own:
+// in earlier waves the keys not above it, in later waves those below it.
+__global__ __launch_bounds__(kPart) void sort_part_kernel(const int64_t *__restrict__ ids, int n,
+                                                          int64_t table_rows, uint2 *__restrict__ out,
+                                                          int parts, Sums s, Zero z) {
+  __shared__ __align__(16) uint32_t keys[kPart];
+  if (zero_block<kPart>(s, z, parts)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int p0 = blockIdx.x * kPart;
-  const int count = min(kPart, n - p0);
-  // item i of the thread is position first + 64 i of the part
-  const int first = wave * 64 * kPartItems + lane;
-  uint32_t key[kPartItems], rank[kPartItems];
-  uint16_t idx[kPartItems];
+  const bool in = p0 + tid < n;
+  // behind the end: above every key, so that it comes before none
+  const uint32_t key = in ? key_of(ids[p0 + tid], table_rows) : UINT32_MAX;
+  keys[tid] = key;
+  __syncthreads();
+  uint32_t before = 0;
 #pragma unroll
-  for (int i = 0; i < kPartItems; ++i) {
-    const int p = first + 64 * i;
-    key[i] = p < count ? key_of(ids[p0 + p], table_rows) : 0u;
-    idx[i] = (uint16_t)p;
-  }
-  for (int shift = 0; shift < bits; shift += kPartBits) {
-    for (int d = lane; d < (1 << kPartBits); d += 64) cnt[wave][d] = 0u;
-    __syncthreads();
-    wave_ranks<kPartBits, kPartItems>(cnt[wave], kPartBits, [&](int i) { return (key[i] >> shift) & ((1u << kPartBits) - 1u); },
-                                      [&](int i) { return first + 64 * i < count; }, rank);
-    __syncthreads();
-    uint32_t c[kWaves], sum = 0, total;      // thread t looks after digit t
+  for (int w = 0; w < kPart / 64; ++w) {
+    const uint32_t bound = key + (w < wave ? 1u : 0u);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      c[w] = cnt[w][tid];
-      sum += c[w];
-    }
-    uint32_t base = block_scan(sum, part, total);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      cnt[w][tid] = base;
-      base += c[w];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPartItems; ++i) {
-      if (first + 64 * i < count) {
-        const uint32_t d = (key[i] >> shift) & ((1u << kPartBits) - 1u);
-        const uint32_t to = cnt[wave][d] + rank[i];
-        keys[to] = key[i];
-        order[to] = idx[i];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPartItems; ++i) {
-      const int p = first + 64 * i;
-      if (p < count) {
-        key[i] = keys[p];
-        idx[i] = order[p];
-      }
+    for (int q = 0; q < 16; ++q) {
+      const uint4 k = reinterpret_cast<const uint4 *>(keys)[w * 16 + q];
+      before += (k.x < bound ? 1u : 0u) + (k.y < bound ? 1u : 0u) + (k.z < bound ? 1u : 0u) +
+                (k.w < bound ? 1u : 0u);
     }
   }
+  // equal keys of the own wave, in the order of the lanes
 #pragma unroll
-  for (int i = 0; i < kPartItems; ++i) {
-    const int p = first + 64 * i;
-    if (p < count) out[p0 + p] = make_uint2(key[i], (uint32_t)(p0 + idx[i]));
+  for (int l = 0; l < 64; ++l) {
+    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, l);
+    before += k == key && l < lane ? 1u : 0u;
   }
+  if (in) out[p0 + before] = make_uint2(key, (uint32_t)(p0 + tid));
 }
-static_assert(kPartThreads == 1 << kPartBits, "one thread per digit");
 
 // Each block places kMergeElems elements of the sorted parts. Thread (q, e) finds how
-// many keys of part q (and of part q + 16) come before element e: an equal key of
+// many keys of parts q, q + 16, ... come before element e: an equal key of
 // an earlier part does, one of a later part does not.
 __global__ __launch_bounds__(kMergeThreads) void merge_parts_kernel(const uint2 *__restrict__ in, int n,
-                                                                    uint2 *__restrict__ out) {
+                                                                    uint2 *__restrict__ out, int blocks,
+                                                                    Sums s, Zero z) {
   __shared__ uint32_t keys[kSmall];
   __shared__ uint32_t place[kMergeElems];
+  if (zero_block<kMergeThreads>(s, z, blocks)) return;
   const int tid = threadIdx.x;
   const int e = blockIdx.x * kMergeElems + (tid & (kMergeElems - 1));
   if (tid < kMergeElems) place[tid] = (uint32_t)(e % kPart);
@@ -287,59 +257,6 @@ __global__ __launch_bounds__(kMergeThreads) void merge_parts_kernel(const uint2 
   if (tid < kMergeElems && e < n) out[place[tid]] = in[e];
 }
 static_assert(kPart % kMergeElems == 0, "a merge block stays within one part");
-
-// The runs of up to kSmall sorted ids, by one block.
-__global__ __launch_bounds__(kRunThreads) void small_runs_kernel(int n, int64_t table_rows, Runs r, Sums s) {
-  __shared__ uint32_t keys[kSmall];
-  __shared__ uint32_t part[17];
-  __shared__ uint32_t kept;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int items = (n + kRunThreads - 1) / kRunThreads;
-  const int first = wave * 64 * items + lane;    // item i is position first + 64 i
-  if (tid == 0) kept = (uint32_t)n;
-#pragma unroll 8
-  for (int p = tid; p < n; p += kRunThreads) keys[p] = r.pairs[p].x;
-  __syncthreads();
-  const auto load = [&](int p, uint32_t &key, bool &edge) {
-    key = p < n ? keys[p] : (uint32_t)table_rows;
-    edge = p < n && (p == 0 || keys[p - 1] != key);
-  };
-  uint32_t heads = 0;
-#pragma unroll 4
-  for (int i = 0; i < items; ++i) {
-    uint32_t key;
-    bool edge;
-    load(first + 64 * i, key, edge);
-    heads += (uint32_t)__popcll(__ballot(edge && key < (uint32_t)table_rows));
-  }
-  uint32_t runs;
-  uint32_t at = block_scan(lane == 0 ? heads : 0u, part, runs);
-  at = (uint32_t)__shfl((int)at, 0, engram::kWave);
-#pragma unroll 4
-  for (int i = 0; i < items; ++i) {
-    const int p = first + 64 * i;
-    uint32_t key;
-    bool edge;
-    load(p, key, edge);
-    const bool valid = key < (uint32_t)table_rows;
-    const uint64_t vote = __ballot(edge && valid);
-    const uint32_t upto = at + (uint32_t)lanes_below(vote) + (edge && valid ? 1u : 0u);
-    at += (uint32_t)__popcll(vote);
-    if (edge && valid) {
-      r.starts[upto - 1] = (uint32_t)p;
-      if (s.rows != nullptr) s.rows[upto - 1] = (int64_t)key;
-    }
-    if (p < n && valid && (p & (r.chunk - 1)) == 0) r.chunk_run[p >> r.chunk_log2] = upto - 1;
-    if (edge && !valid) kept = (uint32_t)p;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    r.starts[runs] = kept;
-    r.meta[0] = runs;
-    r.meta[1] = kept;
-    if (s.count != nullptr) s.count[0] = (int64_t)runs;
-  }
-}
 
 // ---- the sort of more ids: histogram, scan, scatter per digit ---------------------
 // Block b of a pass owns a contiguous range of tiles; counts[b * digits + d] is
@@ -477,58 +394,37 @@ __global__ __launch_bounds__(kSortThreads) void sort_scatter_kernel(
   }
 }
 
-// Runs of the sorted keys: the heads of each tile, then their numbers. Item i of a
-// thread is position first + 64 i, so a wave's positions are contiguous.
-constexpr int kHeadThreads = 512;
-constexpr int kHeadItems = 8;
-constexpr int kHeadTile = kHeadThreads * kHeadItems;
-
+// ---- the runs ----------------------------------------------------------------------
+// Item i of a thread is position first + 64 i, so a wave's positions are contiguous.
+template <int ITEMS>
 __device__ __forceinline__ void load_heads(const uint2 *pairs, int64_t n, int64_t first, uint32_t none,
-                                           uint32_t (&key)[kHeadItems], uint32_t (&before)[kHeadItems]) {
+                                           uint32_t (&key)[ITEMS], uint32_t (&before)[ITEMS]) {
 #pragma unroll
-  for (int i = 0; i < kHeadItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const int64_t p = first + 64 * i;
     key[i] = p < n ? pairs[p].x : none;
     before[i] = p > 0 && p < n ? pairs[p - 1].x : ~key[i];
   }
 }
 
-__global__ __launch_bounds__(kHeadThreads) void count_heads_kernel(
-    const uint2 *__restrict__ pairs, int64_t n, int64_t table_rows, uint32_t *__restrict__ tile_heads) {
-  __shared__ uint32_t part[17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t key[kHeadItems], before[kHeadItems], heads = 0, total;
-  load_heads(pairs, n, (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane,
-             (uint32_t)table_rows, key, before);
+// The runs that begin in this block's tile, `earlier` runs beginning before it.
+template <int ITEMS>
+__device__ __forceinline__ void write_runs(int64_t n, int64_t first, uint32_t table_rows, uint32_t earlier,
+                                           const uint32_t (&key)[ITEMS], const uint32_t (&before)[ITEMS],
+                                           const Runs &r, const Sums &s, uint32_t *part) {
+  const int lane = threadIdx.x & 63;
+  uint32_t heads = 0, total;
 #pragma unroll
-  for (int i = 0; i < kHeadItems; ++i)
-    heads += key[i] < (uint32_t)table_rows && before[i] != key[i] ? 1u : 0u;
-  block_scan(heads, part, total);
-  if (threadIdx.x == 0) tile_heads[blockIdx.x] = total;
-}
-
-__global__ __launch_bounds__(kHeadThreads) void write_runs_kernel(
-    int64_t n, int64_t table_rows, const uint32_t *__restrict__ tile_heads, Runs r, Sums s) {
-  __shared__ uint32_t part[17];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t first = (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane;
-  uint32_t key[kHeadItems], before[kHeadItems];
-  load_heads(r.pairs, n, first, (uint32_t)table_rows, key, before);
-  uint32_t v = 0, tiles_before, total;
-  for (int64_t t = threadIdx.x; t < (int64_t)blockIdx.x; t += kHeadThreads) v += tile_heads[t];
-  block_scan(v, part, tiles_before);             // runs that begin before this tile
-  uint32_t heads = 0;
-#pragma unroll
-  for (int i = 0; i < kHeadItems; ++i)
-    heads += (uint32_t)__popcll(__ballot(key[i] < (uint32_t)table_rows && before[i] != key[i]));
+  for (int i = 0; i < ITEMS; ++i)
+    heads += (uint32_t)__popcll(__ballot(key[i] < table_rows && before[i] != key[i]));
   uint32_t at = block_scan(lane == 0 ? heads : 0u, part, total);
-  at = tiles_before + (uint32_t)__shfl((int)at, 0, engram::kWave);
+  at = earlier + (uint32_t)__shfl((int)at, 0, engram::kWave);
 #pragma unroll
-  for (int i = 0; i < kHeadItems; ++i) {
+  for (int i = 0; i < ITEMS; ++i) {
     const int64_t p = first + 64 * i;
     const bool in = p < n;
     const bool edge = in && before[i] != key[i];
-    const bool valid = key[i] < (uint32_t)table_rows;
+    const bool valid = key[i] < table_rows;
     const uint64_t vote = __ballot(edge && valid);
     const uint32_t upto = at + (uint32_t)lanes_below(vote) + (edge && valid ? 1u : 0u);
     at += (uint32_t)__popcll(vote);
@@ -547,6 +443,65 @@ __global__ __launch_bounds__(kHeadThreads) void write_runs_kernel(
       if (s.count != nullptr) s.count[0] = (int64_t)upto;
     }
   }
+}
+
+// Up to kSmall sorted ids: each block counts the heads before its tile itself.
+constexpr int kSmallTile = 1024;
+__global__ __launch_bounds__(kSmallTile) void small_runs_kernel(int n, int64_t table_rows, Runs r,
+                                                                int blocks, Sums s, Zero z) {
+  __shared__ uint32_t part[17];
+  if (zero_block<kSmallTile>(s, z, blocks)) return;
+  const int tid = threadIdx.x;
+  const uint32_t none = (uint32_t)table_rows;
+  if (n == 0) {
+    if (tid == 0) {
+      r.meta[0] = r.meta[1] = 0u;
+      if (s.count != nullptr) s.count[0] = 0;
+    }
+    return;
+  }
+  const int64_t tile = (int64_t)blockIdx.x * kSmallTile;
+  uint32_t key[1], before[1], heads = 0, earlier;
+  load_heads<1>(r.pairs, n, tile + tid, none, key, before);
+#pragma unroll 8
+  for (int64_t p = tid; p < tile; p += kSmallTile) {
+    const uint32_t k = r.pairs[p].x, b = p > 0 ? r.pairs[p - 1].x : ~k;
+    heads += k < none && b != k ? 1u : 0u;
+  }
+  block_scan(heads, part, earlier);
+  write_runs<1>(n, tile + tid, none, earlier, key, before, r, s, part);
+}
+
+// More: the heads of each tile, then their numbers.
+constexpr int kHeadThreads = 512;
+constexpr int kHeadItems = 8;
+constexpr int kHeadTile = kHeadThreads * kHeadItems;
+
+__global__ __launch_bounds__(kHeadThreads) void count_heads_kernel(
+    const uint2 *__restrict__ pairs, int64_t n, int64_t table_rows, uint32_t *__restrict__ tile_heads) {
+  __shared__ uint32_t part[17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t key[kHeadItems], before[kHeadItems], heads = 0, total;
+  load_heads<kHeadItems>(pairs, n, (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane,
+                         (uint32_t)table_rows, key, before);
+#pragma unroll
+  for (int i = 0; i < kHeadItems; ++i)
+    heads += key[i] < (uint32_t)table_rows && before[i] != key[i] ? 1u : 0u;
+  block_scan(heads, part, total);
+  if (threadIdx.x == 0) tile_heads[blockIdx.x] = total;
+}
+
+__global__ __launch_bounds__(kHeadThreads) void write_runs_kernel(
+    int64_t n, int64_t table_rows, const uint32_t *__restrict__ tile_heads, Runs r, Sums s) {
+  __shared__ uint32_t part[17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t first = (int64_t)blockIdx.x * kHeadTile + wave * 64 * kHeadItems + lane;
+  uint32_t key[kHeadItems], before[kHeadItems];
+  load_heads<kHeadItems>(r.pairs, n, first, (uint32_t)table_rows, key, before);
+  uint32_t v = 0, earlier;
+  for (int64_t t = threadIdx.x; t < (int64_t)blockIdx.x; t += kHeadThreads) v += tile_heads[t];
+  block_scan(v, part, earlier);
+  write_runs<kHeadItems>(n, first, (uint32_t)table_rows, earlier, key, before, r, s, part);
 }
 
 // ---- the sums ----------------------------------------------------------------------
@@ -885,28 +840,40 @@ hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
   const bool dense = n_rows == nullptr;
   const Sums s{grad, a.grad_ld, grad_rows, n_rows, dense ? 1 : 0, accumulate};
   const bool zero_vec = a.dim % 4 == 0 && a.grad_ld % 4 == 0;
-  Zero z{EngramFastDiv(zero_vec ? a.dim / 4 : a.dim), 0, zero_vec, zero_vec && a.grad_ld == a.dim};
-  if (dense && !accumulate) z.total = a.table_rows * z.groups.d;
-  // clearing: 8192 blocks of 256 threads at most
-  const int64_t zero_want = (z.total + 256 * 4 - 1) / (256 * 4);
-  const unsigned zero_blocks = (unsigned)(zero_want < 8192 ? zero_want : 8192);
+  Zero z{EngramFastDiv(zero_vec ? a.dim / 4 : a.dim), 0, 0, zero_vec, zero_vec && a.grad_ld == a.dim};
+  const int64_t zero_total = dense && !accumulate ? a.table_rows * z.groups.d : 0;
+  // blocks that clear the groups [z.begin, z.end), 8 M groups in one go at most
+  const auto zero_blocks = [&](int threads) {
+    const int64_t want = (z.end - z.begin + threads * 4 - 1) / (threads * 4);
+    const int64_t most = ((int64_t)2 << 20) / threads;
+    return (unsigned)(want < most ? want : most);
+  };
   Runs r{pairs[1], (uint32_t *)(ws + p.starts), (uint32_t *)(ws + p.chunk_run),
          (uint32_t *)(ws + p.meta), p.chunk, __builtin_ctz(p.chunk), p.longest};
   if (p.n <= kSmall) {
     const int parts = (int)((p.n + kPart - 1) / kPart);
+    const int merges = parts > 1 ? (int)((p.n + kMergeElems - 1) / kMergeElems) : 0;
+    const int tiles = p.n > 0 ? (int)((p.n + kSmallTile - 1) / kSmallTile) : 1;
     uint2 *sorted = pairs[parts > 1 ? 0 : 1];
-    if (parts + zero_blocks > 0)
-      hipLaunchKernelGGL(sort_part_kernel, dim3((unsigned)parts + zero_blocks), dim3(kPartThreads), 0,
-                         stream, row_ids, (int)p.n, a.table_rows, p.bits, sorted, parts, s, z);
-    if (parts > 1)
-      hipLaunchKernelGGL(merge_parts_kernel,
-                         dim3((unsigned)((p.n + kMergeElems - 1) / kMergeElems)), dim3(kMergeThreads), 0,
-                         stream, (const uint2 *)sorted, (int)p.n, pairs[1]);
-    hipLaunchKernelGGL(small_runs_kernel, dim3(1), dim3(kRunThreads), 0, stream, (int)p.n, a.table_rows,
-                       r, s);
+    z.end = zero_total / 3;
+    if (parts + zero_blocks(kPart) > 0)
+      hipLaunchKernelGGL(sort_part_kernel, dim3((unsigned)parts + zero_blocks(kPart)), dim3(kPart), 0,
+                         stream, row_ids, (int)p.n, a.table_rows, sorted, parts, s, z);
+    z.begin = z.end;
+    if (merges > 0) {
+      z.end = zero_total / 3 * 2;
+      hipLaunchKernelGGL(merge_parts_kernel, dim3((unsigned)merges + zero_blocks(kMergeThreads)),
+                         dim3(kMergeThreads), 0, stream, (const uint2 *)sorted, (int)p.n, pairs[1], merges,
+                         s, z);
+      z.begin = z.end;
+    }
+    z.end = zero_total;
+    hipLaunchKernelGGL(small_runs_kernel, dim3((unsigned)tiles + zero_blocks(kSmallTile)),
+                       dim3(kSmallTile), 0, stream, (int)p.n, a.table_rows, r, tiles, s, z);
   } else {
-    if (zero_blocks > 0)
-      hipLaunchKernelGGL(zero_grad_kernel, dim3(zero_blocks), dim3(256), 0, stream, s, z);
+    z.end = zero_total;
+    if (z.end > 0)
+      hipLaunchKernelGGL(zero_grad_kernel, dim3(zero_blocks(256)), dim3(256), 0, stream, s, z);
     Pass pass = p.pass;
     int at = 1;                       // the next pass writes pairs[1 - at]
     for (int i = 0; i < p.passes; ++i) {
