@@ -410,8 +410,224 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
   wide_store_lines(acc, kv, op.M, op.N, m0, n0, e0);
 }
 
+// ---- up to 256 tokens: columns dealt to every CU, the weight streamed far ahead ------
+// A block takes 128 MT tokens against 32 NI weight rows over the whole of K, so the
+// weight crosses HBM once per token tile. Wave w owns tokens [32 MT w, 32 MT (w + 1))
+// and all the rows. K-steps of 128 inputs; both operands go global -> LDS by direct
+// loads into rings of their own: the weight, which comes from HBM, kRw steps deep, e,
+// which every block reads and L2 holds, kRe. The one barrier of a step stands before its
+// last MFMAs: by then the step's slots have been read and take the loads of step
+// kt + kRw and kt + kRe, and step kt + 1 has landed (loads complete in order: all but
+// the kRe - 2 latest batches, and the scales where they were requested among those).
+// Scales go straight to registers, 16 bytes of a row (4 steps) at a time and a group
+// ahead.
+template <int EF>
+struct SkinnyCfg {
+  static constexpr int kERow = EF == kFp4 ? 64 : 128;   // bytes of an e row and step
+  static constexpr int kRe = EF == kFp4 ? 4 : 3;
+  static constexpr int kRw = EF == kFp4 ? 8 : 6;
+  static constexpr int kUnroll = EF == kFp4 ? 8 : 12;   // a multiple of both rings and of 4
+};
+
+template <int EF, int NI, int MT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
+  using Cfg = SkinnyCfg<EF>;
+  constexpr int kRe = Cfg::kRe, kRw = Cfg::kRw, kERow = Cfg::kERow;
+  constexpr int kRows = 32 * NI, kToks = 128 * MT;
+  constexpr int kWLoads = kRows * 64 / 1024 / 4;        // direct loads of a wave and step
+  constexpr int kELoads = kToks * kERow / 1024 / 4;
+  constexpr int kERows = 1024 / kERow;                  // e rows of a direct load
+  constexpr int kBatch = kWLoads + kELoads;
+  static_assert(NI % 2 == 0, "a wave's share of the weight rows is whole direct loads");
+  // The compiler tells direct loads into different LDS variables apart, for up to eight
+  // of them: one per e slot, and one per two weight slots half a ring apart.
+  constexpr int kWSlot = kRows * 64;
+  __shared__ __align__(1024) uint8_t w0[2 * kWSlot], w1[2 * kWSlot], w2[2 * kWSlot];
+  __shared__ __align__(1024) uint8_t w3[EF == kFp4 ? 2 * kWSlot : 16];
+  __shared__ __align__(1024) uint8_t e0[kToks * kERow], e1[kToks * kERow], e2[kToks * kERow];
+  __shared__ __align__(1024) uint8_t e3[EF == kFp4 ? kToks * kERow : 16];
+  const int n0 = (int)(blockIdx.x % tiles_n) * kRows, m0 = (int)(blockIdx.x / tiles_n) * kToks;
+  const int KB = op.K / 32, KT = op.K / 128;
+  const int w_ld = op.K / 2, e_ld = EF == kFp4 ? op.K / 2 : op.K;
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int frow = lane & 31, h = lane >> 5;
+  const int rows_w = min(kRows, op.N - n0), rows_e = min(kToks, op.M - m0);
+  const __amdgpu_buffer_rsrc_t rsW = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.w_codes + (int64_t)n0 * w_ld), 0, rows_w * w_ld, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsE = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.e_codes + (int64_t)m0 * e_ld), 0, rows_e * e_ld, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsWs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.w_scales + (int64_t)n0 * KB), 0, rows_w * KB, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t rsEs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t *>(op.e_scales + (int64_t)m0 * KB), 0, rows_e * KB, kBufferFlags);
+  // 64-byte rows: chunk c of row r in slot c ^ (r / 2) % 4; 128-byte rows: c ^ f(r)
+  const int c64 = (lane & 3) ^ ((lane >> 3) & 3), c128 = (lane & 7) ^ (lane >> 3);
+  const int w_v = (wave * (kRows / 4) + (lane >> 2)) * w_ld + c64 * 16;
+  const int e_v0 = EF == kFp4 ? (wave * (kToks / 4) + (lane >> 2)) * e_ld + c64 * 16
+                              : (wave * (kToks / 4) + (lane >> 3)) * e_ld + c128 * 16;
+  const int e_v1 = EF == kFp4 ? e_v0 : (wave * (kToks / 4) + (lane >> 3)) * e_ld + (c128 ^ 1) * 16;
+  const int a_sw = (frow >> 1) & 3;
+  const int b_sw = EF == kFp4 ? a_sw : (frow & 7) ^ ((frow >> 3) & 1);
+  const int a_base = frow * 64, b_base = (wave * 32 * MT + frow) * kERow;
+  const int ws_v = frow * KB, es_v = (wave * 32 * MT + frow) * KB;
+
+#define MK_W(s) (((s) % (kRw / 2) == 0 ? w0 : (s) % (kRw / 2) == 1 ? w1 : (s) % (kRw / 2) == 2 ? w2 : w3) + \
+                 (s) / (kRw / 2) * kWSlot)
+#define MK_E(s) ((s) == 0 ? e0 : (s) == 1 ? e1 : (s) == 2 ? e2 : e3)
+#define MK_LDS(p) ((__attribute__((address_space(3))) void *)(p))
+#define MK_LOADW(kt_, s)                                                                       \
+  _Pragma("unroll") for (int i = 0; i < kWLoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
+      rsW, MK_LDS(&MK_W(s)[(wave * kWLoads + i) * 1024]), 16, w_v, i * 16 * w_ld + (kt_) * 64, 0, 0);
+#define MK_LOADE(kt_, s)                                                                       \
+  _Pragma("unroll") for (int i = 0; i < kELoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
+      rsE, MK_LDS(&MK_E(s)[(wave * kELoads + i) * 1024]), 16, (i & 1) ? e_v1 : e_v0,           \
+      i * kERows * e_ld + (kt_) * kERow, 0, 0);
+#define MK_SCALES(g)                                                                           \
+  _Pragma("unroll") for (int i = 0; i < NI; ++i) wsn[i] = load16(rsWs, ws_v, i * 32 * KB + (g) * 16); \
+  _Pragma("unroll") for (int j = 0; j < MT; ++j) esn[j] = load16(rsEs, es_v, j * 32 * KB + (g) * 16);
+#define MK_WORD(v, q) ((q) == 0 ? (v).x : (q) == 1 ? (v).y : (q) == 2 ? (v).z : (v).w)
+#define MK_CHUNK(buf, off, c, sw) (*reinterpret_cast<const uint4 *>(&(buf)[(off) + (((c) ^ (sw)) << 4)]))
+// fragments of sub-step s (0, 1): this half's block 2 h + s of the step's four
+#define MK_FRAGS(u, s, fa, fb)                                                                 \
+  _Pragma("unroll") for (int i = 0; i < NI; ++i)                                               \
+    fa[i] = fp4_operand(MK_CHUNK(MK_W((u) % kRw), a_base + i * 32 * 64, 2 * h + (s), a_sw));   \
+  _Pragma("unroll") for (int j = 0; j < MT; ++j)                                               \
+    fb[j] = EF == kFp4                                                                         \
+                ? fp4_operand(MK_CHUNK(MK_E((u) % kRe), b_base + j * 32 * kERow, 2 * h + (s), b_sw)) \
+                : fp8_operand(MK_CHUNK(MK_E((u) % kRe), b_base + j * 32 * kERow, 2 * (s) + h, b_sw), \
+                              MK_CHUNK(MK_E((u) % kRe), b_base + j * 32 * kERow, 4 + 2 * (s) + h, b_sw));
+#define MK_MFMA(s, fa, fb)                                                                     \
+  _Pragma("unroll") for (int i = 0; i < NI; ++i) _Pragma("unroll") for (int j = 0; j < MT; ++j) \
+    acc[i][j] = mfma_unit<EF, s>(fa[i], fb[j], acc[i][j], sa[i], sb[j]);
+#define MK_FENCE() __builtin_amdgcn_sched_barrier(0)
+#define MK_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier(mask, n, 0)
+
+  f32x16 acc[NI][MT];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  i32x8 fa0[NI], fb0[MT], fa1[NI], fb1[MT];
+  uint4 ws[NI], es[MT], wsn[NI], esn[MT];
+  uint32_t sa[NI], sb[MT];
+  MK_SCALES(0)
+#pragma unroll
+  for (int i = 0; i < NI; ++i) ws[i] = wsn[i];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) es[j] = esn[j];
+  MK_LOADW(0, 0) MK_LOADE(0, 0)
+  MK_LOADW(1, 1) MK_LOADE(1, 1)
+  MK_LOADW(2, 2) MK_LOADE(2, 2)
+  if constexpr (EF == kFp4) {
+    MK_LOADW(3, 3) MK_LOADE(3, 3)
+    MK_LOADW(4, 4) MK_LOADW(5, 5) MK_LOADW(6, 6) MK_LOADW(7, 7)
+  } else {
+    MK_LOADW(3, 3) MK_LOADW(4, 4) MK_LOADW(5, 5)
+  }
+  // step 0 has landed when only what was issued after it is outstanding
+  if constexpr (EF == kFp4)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(3 * kBatch + 4 * kWLoads) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kBatch + 3 * kWLoads) : "memory");
+  MK_FENCE();
+  MK_FRAGS(0, 0, fa0, fb0)
+// Step kt + u. The LDS reads come before the direct loads of the same step, whose
+// slots the compiler believes to be in flight (it cannot see the barrier's wait).
+#define MK_STEP(u)                                                                             \
+  if (kt + (u) < KT) {                                                                         \
+    if ((u) % 4 == 0) { MK_SCALES((kt + (u)) / 4 + 1) }                                        \
+    _Pragma("unroll") for (int i = 0; i < NI; ++i) sa[i] = MK_WORD(ws[i], (u) % 4) >> (16 * h); \
+    _Pragma("unroll") for (int j = 0; j < MT; ++j) sb[j] = MK_WORD(es[j], (u) % 4) >> (16 * h); \
+    MK_FRAGS(u, 1, fa1, fb1)                                                                   \
+    MK_MFMA(0, fa0, fb0)                                                                       \
+    MK_FENCE();                                                                                \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(                         \
+                     (kRe - 2) * kBatch + ((u) % 4 <= kRe - 3 ? NI + MT : 0)) : "memory");     \
+    MK_FENCE();                                                                                \
+    MK_FRAGS((u) + 1, 0, fa0, fb0)                                                             \
+    MK_FENCE();                                                                                \
+    MK_LOADW(kt + (u) + kRw, (u) % kRw)                                                        \
+    MK_LOADE(kt + (u) + kRe, (u) % kRe)                                                        \
+    MK_MFMA(1, fa1, fb1)                                                                       \
+    _Pragma("unroll") for (int g_ = 0; g_ < kBatch; ++g_) { MK_GROUP(0x008, 1); MK_GROUP(0x020, 2); } \
+    MK_FENCE();                                                                                \
+    if ((u) % 4 == 3) {                                                                        \
+      _Pragma("unroll") for (int i = 0; i < NI; ++i) ws[i] = wsn[i];                           \
+      _Pragma("unroll") for (int j = 0; j < MT; ++j) es[j] = esn[j];                           \
+    }                                                                                          \
+  }
+  for (int kt = 0; kt < KT; kt += Cfg::kUnroll) {
+    MK_STEP(0) MK_STEP(1) MK_STEP(2) MK_STEP(3) MK_STEP(4) MK_STEP(5) MK_STEP(6) MK_STEP(7)
+    if constexpr (Cfg::kUnroll == 12) { MK_STEP(8) MK_STEP(9) MK_STEP(10) MK_STEP(11) }
+  }
+  // every direct load has landed before the slots hold the outputs
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#undef MK_STEP
+#undef MK_GROUP
+#undef MK_FENCE
+#undef MK_MFMA
+#undef MK_FRAGS
+#undef MK_CHUNK
+#undef MK_WORD
+#undef MK_SCALES
+#undef MK_LOADE
+#undef MK_LOADW
+#undef MK_LDS
+#undef MK_E
+#undef MK_W
+  // 32 tokens x 32 NI columns of a wave at a time through LDS, as wide_store_lines
+  constexpr int kChunks = 4 * NI;                       // 16-byte chunks of a token
+  constexpr int kPatch = 32 * kChunks * 16;
+  static_assert(EF == kFp4 ? kPatch <= kToks * kERow : 2 * kPatch <= kToks * kERow, "patches fit the e slots");
+  uint8_t *mine = EF == kFp4 ? (wave == 0 ? e0 : wave == 1 ? e1 : wave == 2 ? e2 : e3)
+                             : (wave < 2 ? e0 : e1) + (wave & 1) * kPatch;
+  const int col = n0 + (lane % kChunks) * 8;
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        uint2 v;
+        v.x = engram::pack_bf16x2(acc[i][j][g * 4 + 0], acc[i][j][g * 4 + 1]);
+        v.y = engram::pack_bf16x2(acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]);
+        *reinterpret_cast<uint2 *>(mine + (frow * kChunks + ((i * 4 + g) ^ (frow & (kChunks - 1)))) * 16 +
+                                   h * 8) = v;
+      }
+#pragma unroll
+    for (int q = 0; q < 32 * kChunks / 64; ++q) {
+      const int t = (q * 64 + lane) / kChunks;
+      const engram::u32x4 v = *reinterpret_cast<const engram::u32x4 *>(
+          mine + (t * kChunks + ((lane % kChunks) ^ (t & (kChunks - 1)))) * 16);
+      const int m = m0 + wave * 32 * MT + j * 32 + t;
+      if (m < op.M && col < op.N)
+        __builtin_nontemporal_store(v, reinterpret_cast<engram::u32x4 *>(kv + (int64_t)m * op.N + col));
+    }
+  }
+}
+
+template <int EF, int NI, int MT>
+hipError_t launch_skinny(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
+  const int tiles_n = (op.N + 32 * NI - 1) / (32 * NI), tiles_m = (op.M + 128 * MT - 1) / (128 * MT);
+  hipLaunchKernelGGL((mx4_skinny_kernel<EF, NI, MT>), dim3((unsigned)(tiles_n * tiles_m)), dim3(256), 0,
+                     stream, op, kv, tiles_n);
+  return hipGetLastError();
+}
+
+constexpr int kSkinnyMax = 256;
+
 template <int EF>
 hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
+  if (op.M > 32 && op.M <= kSkinnyMax) {
+    if (op.M <= 128)
+      return op.N >= 16384 ? launch_skinny<EF, 4, 1>(op, kv, stream) : launch_skinny<EF, 2, 1>(op, kv, stream);
+    return op.N >= 16384 ? launch_skinny<EF, 4, 2>(op, kv, stream) : launch_skinny<EF, 2, 2>(op, kv, stream);
+  }
   if (op.M > 64) {
     const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
     hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kWideThreads), 0,
