@@ -414,19 +414,21 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
 // A block takes 128 MT tokens against 32 NI weight rows over the whole of K, so the
 // weight crosses HBM once per token tile. Wave w owns tokens [32 MT w, 32 MT (w + 1))
 // and all the rows. K-steps of 128 inputs; both operands go global -> LDS by direct
-// loads into rings of their own: the weight, which comes from HBM, kRw steps deep, e,
-// which every block reads and L2 holds, kRe. The one barrier of a step stands before its
-// last MFMAs: by then the step's slots have been read and take the loads of step
-// kt + kRw and kt + kRe, and step kt + 1 has landed (loads complete in order: all but
-// the kRe - 2 latest batches, and the scales where they were requested among those).
+// loads into rings of their own: the weight, which comes from HBM, kRw pairs of steps
+// deep (whole cache lines of a row; by the step, in half lines, 256 tokens took 52 us
+// for PAIR_US), e, which every block reads and L2 holds, kRe steps. The one barrier of
+// a step stands before its last MFMAs: by then the step's slots have been read and take
+// the loads of the pair kRw ahead and of step kt + kRe, and step kt + 1 has landed
+// (loads complete in order: all but the kRe - 2 latest batches, and the scales where
+// they were requested among those).
 // Scales go straight to registers, 16 bytes of a row (4 steps) at a time and a group
 // ahead.
 template <int EF>
 struct SkinnyCfg {
   static constexpr int kERow = EF == kFp4 ? 64 : 128;   // bytes of an e row and step
   static constexpr int kRe = EF == kFp4 ? 4 : 3;
-  static constexpr int kRw = EF == kFp4 ? 8 : 6;
-  static constexpr int kUnroll = EF == kFp4 ? 8 : 12;   // a multiple of both rings and of 4
+  static constexpr int kRw = EF == kFp4 ? 4 : 3;
+  static constexpr int kUnroll = EF == kFp4 ? 8 : 12;   // steps: a multiple of both rings and of 4
 };
 
 template <int EF, int NI, int MT>
@@ -435,16 +437,13 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   using Cfg = SkinnyCfg<EF>;
   constexpr int kRe = Cfg::kRe, kRw = Cfg::kRw, kERow = Cfg::kERow;
   constexpr int kRows = 32 * NI, kToks = 128 * MT;
-  constexpr int kWLoads = kRows * 64 / 1024 / 4;        // direct loads of a wave and step
-  constexpr int kELoads = kToks * kERow / 1024 / 4;
+  constexpr int kWLoads = kRows * 128 / 1024 / 4;       // direct loads of a wave and pair
+  constexpr int kELoads = kToks * kERow / 1024 / 4;     // of a wave and step
   constexpr int kERows = 1024 / kERow;                  // e rows of a direct load
-  constexpr int kBatch = kWLoads + kELoads;
-  static_assert(NI % 2 == 0, "a wave's share of the weight rows is whole direct loads");
-  // The compiler tells direct loads into different LDS variables apart, for up to eight
-  // of them: one per e slot, and one per two weight slots half a ring apart.
-  constexpr int kWSlot = kRows * 64;
-  __shared__ __align__(1024) uint8_t w0[2 * kWSlot], w1[2 * kWSlot], w2[2 * kWSlot];
-  __shared__ __align__(1024) uint8_t w3[EF == kFp4 ? 2 * kWSlot : 16];
+  constexpr int kSLoads = NI + MT;                      // scale loads of four steps
+  // one LDS variable per slot: the compiler tells direct loads into up to eight apart
+  __shared__ __align__(1024) uint8_t w0[kRows * 128], w1[kRows * 128], w2[kRows * 128];
+  __shared__ __align__(1024) uint8_t w3[EF == kFp4 ? kRows * 128 : 16];
   __shared__ __align__(1024) uint8_t e0[kToks * kERow], e1[kToks * kERow], e2[kToks * kERow];
   __shared__ __align__(1024) uint8_t e3[EF == kFp4 ? kToks * kERow : 16];
   const int n0 = (int)(blockIdx.x % tiles_n) * kRows, m0 = (int)(blockIdx.x / tiles_n) * kToks;
@@ -465,22 +464,23 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
       const_cast<uint8_t *>(op.e_scales + (int64_t)m0 * KB), 0, rows_e * KB, kBufferFlags);
   // 64-byte rows: chunk c of row r in slot c ^ (r / 2) % 4; 128-byte rows: c ^ f(r)
   const int c64 = (lane & 3) ^ ((lane >> 3) & 3), c128 = (lane & 7) ^ (lane >> 3);
-  const int w_v = (wave * (kRows / 4) + (lane >> 2)) * w_ld + c64 * 16;
+  const int w_v0 = (wave * (kRows / 4) + (lane >> 3)) * w_ld + c128 * 16;
+  const int w_v1 = (wave * (kRows / 4) + (lane >> 3)) * w_ld + (c128 ^ 1) * 16;
   const int e_v0 = EF == kFp4 ? (wave * (kToks / 4) + (lane >> 2)) * e_ld + c64 * 16
                               : (wave * (kToks / 4) + (lane >> 3)) * e_ld + c128 * 16;
   const int e_v1 = EF == kFp4 ? e_v0 : (wave * (kToks / 4) + (lane >> 3)) * e_ld + (c128 ^ 1) * 16;
-  const int a_sw = (frow >> 1) & 3;
-  const int b_sw = EF == kFp4 ? a_sw : (frow & 7) ^ ((frow >> 3) & 1);
-  const int a_base = frow * 64, b_base = (wave * 32 * MT + frow) * kERow;
+  const int a_sw = (frow & 7) ^ ((frow >> 3) & 1);
+  const int b_sw = EF == kFp4 ? (frow >> 1) & 3 : a_sw;
+  const int a_base = frow * 128, b_base = (wave * 32 * MT + frow) * kERow;
   const int ws_v = frow * KB, es_v = (wave * 32 * MT + frow) * KB;
 
-#define MK_W(s) (((s) % (kRw / 2) == 0 ? w0 : (s) % (kRw / 2) == 1 ? w1 : (s) % (kRw / 2) == 2 ? w2 : w3) + \
-                 (s) / (kRw / 2) * kWSlot)
+#define MK_W(s) ((s) == 0 ? w0 : (s) == 1 ? w1 : (s) == 2 ? w2 : w3)
 #define MK_E(s) ((s) == 0 ? e0 : (s) == 1 ? e1 : (s) == 2 ? e2 : e3)
 #define MK_LDS(p) ((__attribute__((address_space(3))) void *)(p))
-#define MK_LOADW(kt_, s)                                                                       \
+#define MK_LOADW(pair, s)                                                                      \
   _Pragma("unroll") for (int i = 0; i < kWLoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
-      rsW, MK_LDS(&MK_W(s)[(wave * kWLoads + i) * 1024]), 16, w_v, i * 16 * w_ld + (kt_) * 64, 0, 0);
+      rsW, MK_LDS(&MK_W(s)[(wave * kWLoads + i) * 1024]), 16, (i & 1) ? w_v1 : w_v0,           \
+      i * 8 * w_ld + (pair) * 128, 0, 0);
 #define MK_LOADE(kt_, s)                                                                       \
   _Pragma("unroll") for (int i = 0; i < kELoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
       rsE, MK_LDS(&MK_E(s)[(wave * kELoads + i) * 1024]), 16, (i & 1) ? e_v1 : e_v0,           \
@@ -493,7 +493,8 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
 // fragments of sub-step s (0, 1): this half's block 2 h + s of the step's four
 #define MK_FRAGS(u, s, fa, fb)                                                                 \
   _Pragma("unroll") for (int i = 0; i < NI; ++i)                                               \
-    fa[i] = fp4_operand(MK_CHUNK(MK_W((u) % kRw), a_base + i * 32 * 64, 2 * h + (s), a_sw));   \
+    fa[i] = fp4_operand(MK_CHUNK(MK_W((u) / 2 % kRw), a_base + i * 32 * 128,                   \
+                                 (u) % 2 * 4 + 2 * h + (s), a_sw));                            \
   _Pragma("unroll") for (int j = 0; j < MT; ++j)                                               \
     fb[j] = EF == kFp4                                                                         \
                 ? fp4_operand(MK_CHUNK(MK_E((u) % kRe), b_base + j * 32 * kERow, 2 * h + (s), b_sw)) \
@@ -520,54 +521,59 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   for (int i = 0; i < NI; ++i) ws[i] = wsn[i];
 #pragma unroll
   for (int j = 0; j < MT; ++j) es[j] = esn[j];
-  MK_LOADW(0, 0) MK_LOADE(0, 0)
-  MK_LOADW(1, 1) MK_LOADE(1, 1)
-  MK_LOADW(2, 2) MK_LOADE(2, 2)
-  if constexpr (EF == kFp4) {
-    MK_LOADW(3, 3) MK_LOADE(3, 3)
-    MK_LOADW(4, 4) MK_LOADW(5, 5) MK_LOADW(6, 6) MK_LOADW(7, 7)
-  } else {
-    MK_LOADW(3, 3) MK_LOADW(4, 4) MK_LOADW(5, 5)
-  }
+  MK_LOADW(0, 0) MK_LOADE(0, 0) MK_LOADE(1, 1)
+  MK_LOADW(1, 1) MK_LOADE(2, 2)
+  if constexpr (EF == kFp4) { MK_LOADE(3, 3) }
+  MK_LOADW(2, 2)
+  if constexpr (EF == kFp4) { MK_LOADW(3, 3) }
   // step 0 has landed when only what was issued after it is outstanding
-  if constexpr (EF == kFp4)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(3 * kBatch + 4 * kWLoads) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kBatch + 3 * kWLoads) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kRe - 1) * kELoads + (kRw - 1) * kWLoads)
+               : "memory");
   MK_FENCE();
   MK_FRAGS(0, 0, fa0, fb0)
+// What may be outstanding at step u's barrier: the batches of the kRe - 2 steps before
+// it, the weight's among them (issued at odd steps), and the scales (at every fourth).
+#define MK_PENDING(u)                                                                            ((kRe - 2) * kELoads + (kRe == 4 || (u) % 2 == 0 ? kWLoads : 0) + ((u) % 4 <= kRe - 3 ? kSLoads : 0))
 // Step kt + u. The LDS reads come before the direct loads of the same step, whose
 // slots the compiler believes to be in flight (it cannot see the barrier's wait).
 #define MK_STEP(u)                                                                             \
-  if (kt + (u) < KT) {                                                                         \
+  {                                                                                            \
     if ((u) % 4 == 0) { MK_SCALES((kt + (u)) / 4 + 1) }                                        \
     _Pragma("unroll") for (int i = 0; i < NI; ++i) sa[i] = MK_WORD(ws[i], (u) % 4) >> (16 * h); \
     _Pragma("unroll") for (int j = 0; j < MT; ++j) sb[j] = MK_WORD(es[j], (u) % 4) >> (16 * h); \
     MK_FRAGS(u, 1, fa1, fb1)                                                                   \
     MK_MFMA(0, fa0, fb0)                                                                       \
     MK_FENCE();                                                                                \
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(                         \
-                     (kRe - 2) * kBatch + ((u) % 4 <= kRe - 3 ? NI + MT : 0)) : "memory");     \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(MK_PENDING(u)) : "memory"); \
     MK_FENCE();                                                                                \
     MK_FRAGS((u) + 1, 0, fa0, fb0)                                                             \
     MK_FENCE();                                                                                \
-    MK_LOADW(kt + (u) + kRw, (u) % kRw)                                                        \
+    if ((u) % 2 == 1) { MK_LOADW((kt + (u)) / 2 + kRw, (u) / 2 % kRw) }                        \
     MK_LOADE(kt + (u) + kRe, (u) % kRe)                                                        \
     MK_MFMA(1, fa1, fb1)                                                                       \
-    _Pragma("unroll") for (int g_ = 0; g_ < kBatch; ++g_) { MK_GROUP(0x008, 1); MK_GROUP(0x020, 2); } \
+    _Pragma("unroll") for (int g_ = 0; g_ < 8; ++g_) { MK_GROUP(0x008, 1); MK_GROUP(0x020, 2); } \
     MK_FENCE();                                                                                \
     if ((u) % 4 == 3) {                                                                        \
       _Pragma("unroll") for (int i = 0; i < NI; ++i) ws[i] = wsn[i];                           \
       _Pragma("unroll") for (int j = 0; j < MT; ++j) es[j] = esn[j];                           \
     }                                                                                          \
   }
-  for (int kt = 0; kt < KT; kt += Cfg::kUnroll) {
+// The steps behind the last whole unrolling stand apart: branches around steps of the
+// main loop made the compiler wait for every load at each of them.
+#define MK_LAST(u) \
+  if (kt + (u) < KT) MK_STEP(u)
+  int kt = 0;
+  for (; kt + Cfg::kUnroll <= KT; kt += Cfg::kUnroll) {
     MK_STEP(0) MK_STEP(1) MK_STEP(2) MK_STEP(3) MK_STEP(4) MK_STEP(5) MK_STEP(6) MK_STEP(7)
     if constexpr (Cfg::kUnroll == 12) { MK_STEP(8) MK_STEP(9) MK_STEP(10) MK_STEP(11) }
   }
+  MK_LAST(0) MK_LAST(1) MK_LAST(2) MK_LAST(3) MK_LAST(4) MK_LAST(5) MK_LAST(6)
+  if constexpr (Cfg::kUnroll == 12) { MK_LAST(7) MK_LAST(8) MK_LAST(9) MK_LAST(10) }
   // every direct load has landed before the slots hold the outputs
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#undef MK_LAST
 #undef MK_STEP
+#undef MK_PENDING
 #undef MK_GROUP
 #undef MK_FENCE
 #undef MK_MFMA
