@@ -49,22 +49,25 @@ __device__ __forceinline__ f32x16 mfma_unit(i32x8 w, i32x8 e, f32x16 acc, uint32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, e, acc, kFp4, EF, I, (int)ws, I, (int)es);
 }
 
-// ---- a few tokens: the weight straight from memory to registers -------------------
-// A block takes 32 weight rows against 32 MT tokens; its waves split the inputs
+// ---- few tokens and few columns: the weight straight from memory to registers --------
+// A block takes 32 weight rows against up to 32 tokens; its waves split the inputs
 // (unit u belongs to wave u % waves) and their sums meet in LDS in wave order. Each
-// weight byte is loaded once, by the lane that multiplies it.
+// weight byte is loaded once, by the lane that multiplies it. With so few rows that
+// every CU has one block at most, splitting K over the waves beats the next kernel's
+// long pipeline (5120 x 6144 at 1 token: 7.7 against 11.1 us, 12800 x 6144: 12.9
+// against 11.8).
 constexpr int kThinWaves = 4;
 
-template <int EF, int MT>
+template <int EF>
 struct ThinUnit {
   uint4 w[4];
-  uint4 e[MT][EF == kFp4 ? 4 : 8];
-  uint32_t ws, es[MT];
+  uint4 e[EF == kFp4 ? 4 : 8];
+  uint32_t ws, es;
 };
 
-template <int EF, int MT>
-__device__ __forceinline__ void thin_load(ThinUnit<EF, MT> &t, const Mx4Operands &op, int unit,
-                                          int n, const int (&m)[MT], int h) {
+template <int EF>
+__device__ __forceinline__ void thin_load(ThinUnit<EF> &t, const Mx4Operands &op, int unit, int n, int m,
+                                          int h) {
   const int KB = op.K / 32;
   const int b = unit * 8 + 4 * h;
   const bool in = b < KB;
@@ -73,89 +76,70 @@ __device__ __forceinline__ void thin_load(ThinUnit<EF, MT> &t, const Mx4Operands
 #pragma unroll
   for (int i = 0; i < 4; ++i) t.w[i] = in ? reinterpret_cast<const uint4 *>(w)[i] : none;
   t.ws = in ? *reinterpret_cast<const uint32_t *>(op.w_scales + (int64_t)n * KB + b) : 0x7F7F7F7Fu;
+  if (EF == kFp4) {
+    const uint8_t *e = op.e_codes + (int64_t)m * (op.K / 2) + b * 16;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    if (EF == kFp4) {
-      const uint8_t *e = op.e_codes + (int64_t)m[j] * (op.K / 2) + b * 16;
+    for (int i = 0; i < 4; ++i) t.e[i] = in ? reinterpret_cast<const uint4 *>(e)[i] : none;
+  } else {
+    // halves of blocks 8 unit + i and 8 unit + 4 + i
+    const uint8_t *e = op.e_codes + (int64_t)m * op.K + unit * 256 + 16 * h;
+    const bool second = unit * 8 + 4 < KB;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t.e[j][i] = in ? reinterpret_cast<const uint4 *>(e)[i] : none;
-    } else {
-      // halves of blocks 8 unit + i and 8 unit + 4 + i
-      const uint8_t *e = op.e_codes + (int64_t)m[j] * op.K + unit * 256 + 16 * h;
-      const bool second = unit * 8 + 4 < KB;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        t.e[j][2 * i % 8] = *reinterpret_cast<const uint4 *>(e + i * 32);
-        t.e[j][(2 * i + 1) % 8] = second ? *reinterpret_cast<const uint4 *>(e + 128 + i * 32) : none;
-      }
+    for (int i = 0; i < 4; ++i) {
+      t.e[2 * i % 8] = *reinterpret_cast<const uint4 *>(e + i * 32);
+      t.e[(2 * i + 1) % 8] = second ? *reinterpret_cast<const uint4 *>(e + 128 + i * 32) : none;
     }
-    t.es[j] = in ? *reinterpret_cast<const uint32_t *>(op.e_scales + (int64_t)m[j] * KB + b)
-                 : 0x7F7F7F7Fu;
   }
+  t.es = in ? *reinterpret_cast<const uint32_t *>(op.e_scales + (int64_t)m * KB + b) : 0x7F7F7F7Fu;
 }
 
-template <int EF, int MT, int I>
-__device__ __forceinline__ void thin_mfma(f32x16 (&acc)[MT], const ThinUnit<EF, MT> &t) {
-  const i32x8 w = fp4_operand(t.w[I]);
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const i32x8 e = EF == kFp4 ? fp4_operand(t.e[j][I]) : fp8_operand(t.e[j][2 * I % 8], t.e[j][(2 * I + 1) % 8]);
-    acc[j] = mfma_unit<EF, I>(w, e, acc[j], t.ws, t.es[j]);
-  }
+template <int EF, int I>
+__device__ __forceinline__ void thin_mfma(f32x16 &acc, const ThinUnit<EF> &t) {
+  const i32x8 e = EF == kFp4 ? fp4_operand(t.e[I]) : fp8_operand(t.e[2 * I % 8], t.e[(2 * I + 1) % 8]);
+  acc = mfma_unit<EF, I>(fp4_operand(t.w[I]), e, acc, t.ws, t.es);
 }
 
-template <int EF, int MT>
+template <int EF>
 __global__ __launch_bounds__(kThinWaves * 64) void mx4_thin_kernel(Mx4Operands op,
                                                                    uint16_t *__restrict__ kv) {
-  __shared__ float part[kThinWaves - 1][MT * 16][64];
+  __shared__ float part[kThinWaves - 1][16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int row = lane & 31, h = lane >> 5;
-  const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32 * MT;
+  const int n0 = blockIdx.x * 32;
   // rows past the end repeat the last one; their outputs are not stored
-  const int n = min(n0 + row, op.N - 1);
-  int m[MT];
+  const int n = min(n0 + row, op.N - 1), m = min(row, op.M - 1);
+  f32x16 acc;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) m[j] = min(m0 + j * 32 + row, op.M - 1);
-  f32x16 acc[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
   const int units = (op.K + 255) / 256;
   for (int u = wave; u < units; u += kThinWaves) {
-    ThinUnit<EF, MT> t;
-    thin_load<EF, MT>(t, op, u, n, m, h);
-    thin_mfma<EF, MT, 0>(acc, t);
-    thin_mfma<EF, MT, 1>(acc, t);
-    thin_mfma<EF, MT, 2>(acc, t);
-    thin_mfma<EF, MT, 3>(acc, t);
+    ThinUnit<EF> t;
+    thin_load<EF>(t, op, u, n, m, h);
+    thin_mfma<EF, 0>(acc, t);
+    thin_mfma<EF, 1>(acc, t);
+    thin_mfma<EF, 2>(acc, t);
+    thin_mfma<EF, 3>(acc, t);
   }
   if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < MT; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) part[wave - 1][j * 16 + r][lane] = acc[j][r];
+    for (int r = 0; r < 16; ++r) part[wave - 1][r][lane] = acc[r];
   }
   __syncthreads();
   if (wave > 0) return;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
+  for (int w = 0; w < kThinWaves - 1; ++w)
 #pragma unroll
-    for (int w = 0; w < kThinWaves - 1; ++w)
+    for (int r = 0; r < 16; ++r) acc[r] += part[w][r][lane];
+  // accumulator r: column n0 + 8 (r / 4) + 4 h + r % 4 of token `row`
+  if (row >= op.M) return;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[j][r] += part[w][j * 16 + r][lane];
-    // accumulator r: column n0 + 8 (r / 4) + 4 h + r % 4 of token m0 + 32 j + row
-    const int t = m0 + j * 32 + row;
-    if (t >= op.M) continue;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int c = n0 + g * 8 + h * 4;
-      if (c < op.N) {
-        uint2 v;
-        v.x = engram::pack_bf16x2(acc[j][g * 4 + 0], acc[j][g * 4 + 1]);
-        v.y = engram::pack_bf16x2(acc[j][g * 4 + 2], acc[j][g * 4 + 3]);
-        *reinterpret_cast<uint2 *>(kv + (int64_t)t * op.N + c) = v;
-      }
+  for (int g = 0; g < 4; ++g) {
+    const int c = n0 + g * 8 + h * 4;
+    if (c < op.N) {
+      uint2 v;
+      v.x = engram::pack_bf16x2(acc[g * 4 + 0], acc[g * 4 + 1]);
+      v.y = engram::pack_bf16x2(acc[g * 4 + 2], acc[g * 4 + 3]);
+      *reinterpret_cast<uint2 *>(kv + (int64_t)row * op.N + c) = v;
     }
   }
 }
@@ -416,7 +400,7 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
 // and all the rows. K-steps of 128 inputs; both operands go global -> LDS by direct
 // loads into rings of their own: the weight, which comes from HBM, kRw pairs of steps
 // deep (whole cache lines of a row; by the step, in half lines, 256 tokens took 52 us
-// for PAIR_US), e, which every block reads and L2 holds, kRe steps. The one barrier of
+// for 51), e, which every block reads and L2 holds, kRe steps. The one barrier of
 // a step stands before its last MFMAs: by then the step's slots have been read and take
 // the loads of the pair kRw ahead and of step kt + kRe, and step kt + 1 has landed
 // (loads complete in order: all but the kRe - 2 latest batches, and the scales where
@@ -625,42 +609,41 @@ hipError_t launch_skinny(const Mx4Operands &op, uint16_t *kv, hipStream_t stream
   return hipGetLastError();
 }
 
-constexpr int kSkinnyMax = 256;
-
+// Which kernel: up to 32 tokens and one block of 32 rows per CU, the thin one. Up to 256
+// tokens, or where its blocks fit the CUs at once, the skinny one (600 tokens x 5120
+// columns of E4M3: 27 us against 61 in whole tiles; 512 x 25600, two blocks a CU: 84
+// against 73), with 64 weight rows a block where those fit the CUs, else 128, which
+// halves e's traffic. Above, whole 256 x 256 tiles.
 template <int EF>
 hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
-  if (op.M > 32 && op.M <= kSkinnyMax) {
-    if (op.M <= 128)
-      return op.N >= 16384 ? launch_skinny<EF, 4, 1>(op, kv, stream) : launch_skinny<EF, 2, 1>(op, kv, stream);
-    return op.N >= 16384 ? launch_skinny<EF, 4, 2>(op, kv, stream) : launch_skinny<EF, 2, 2>(op, kv, stream);
-  }
-  if (op.M > 64) {
-    const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
-    hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kWideThreads), 0,
-                       stream, op, kv, tiles_m, tiles_n);
+  int cus = 0;
+  const hipError_t err = cu_count(cus);
+  if (err != hipSuccess) return err;
+  if (op.M <= 32 && op.N <= 32 * cus) {
+    hipLaunchKernelGGL((mx4_thin_kernel<EF>), dim3((unsigned)((op.N + 31) / 32)), dim3(kThinWaves * 64), 0,
+                       stream, op, kv);
     return hipGetLastError();
   }
-  const dim3 block(kThinWaves * 64);
-  if (op.M <= 32)
-    hipLaunchKernelGGL((mx4_thin_kernel<EF, 1>), dim3((unsigned)((op.N + 31) / 32)), block, 0, stream, op, kv);
-  else
-    hipLaunchKernelGGL((mx4_thin_kernel<EF, 2>), dim3((unsigned)((op.N + 31) / 32)), block, 0, stream, op, kv);
+  const auto blocks = [&](int rows) {
+    return (int64_t)((op.M + 255) / 256) * ((op.N + rows - 1) / rows);
+  };
+  if (op.M <= 256 || blocks(128) <= cus) {
+    const bool narrow = blocks(64) <= cus;
+    if (op.M <= 128)
+      return narrow ? launch_skinny<EF, 2, 1>(op, kv, stream) : launch_skinny<EF, 4, 1>(op, kv, stream);
+    return narrow ? launch_skinny<EF, 2, 2>(op, kv, stream) : launch_skinny<EF, 4, 2>(op, kv, stream);
+  }
+  const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
+  hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kWideThreads), 0,
+                     stream, op, kv, tiles_m, tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t engram_gemm_mx4_workspace(int64_t m, int64_t n, int64_t k, bool e_fp4, size_t *bytes) {
-  (void)m; (void)n; (void)k; (void)e_fp4;
-  *bytes = 0;
-  return hipSuccess;
-}
-
 hipError_t engram_launch_gemm_mx4(const uint8_t *w_codes, const uint8_t *w_scales,
                                   const uint8_t *e_codes, const uint8_t *e_scales, bool e_fp4,
-                                  uint16_t *kv, int64_t m, int64_t n, int64_t k, void *workspace,
-                                  size_t workspace_bytes, hipStream_t stream) {
-  (void)workspace; (void)workspace_bytes;
+                                  uint16_t *kv, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
   if (m <= 0 || n <= 0) return hipSuccess;
   const Mx4Operands op{w_codes, w_scales, e_codes, e_scales, (int)m, (int)n, (int)k};
   return e_fp4 ? launch_mx4<kFp4>(op, kv, stream) : launch_mx4<kFp8>(op, kv, stream);

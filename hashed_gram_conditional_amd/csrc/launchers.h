@@ -143,6 +143,4 @@ hipError_t engram_launch_quantize_mx4(bool f32, const void *src, int64_t rows, i
 // E4M3 [m, k], scales [.., k / 32]; kv bf16 [m, n].
 hipError_t engram_launch_gemm_mx4(const uint8_t *w_codes, const uint8_t *w_scales,
                                   const uint8_t *e_codes, const uint8_t *e_scales, bool e_fp4,
-                                  uint16_t *kv, int64_t m, int64_t n, int64_t k, void *workspace,
-                                  size_t workspace_bytes, hipStream_t stream);
-hipError_t engram_gemm_mx4_workspace(int64_t m, int64_t n, int64_t k, bool e_fp4, size_t *bytes);
+                                  uint16_t *kv, int64_t m, int64_t n, int64_t k, hipStream_t stream);

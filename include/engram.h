@@ -763,8 +763,9 @@ int engram_quantize_mx4(const void *src, int32_t src_type, int64_t rows, int64_t
  *   kv        bf16 [tokens, out_dim], 16-byte aligned
  *   in_dim    a multiple of 128, at most 2^20; out_dim % 8 == 0; the tile bound of
  *             engram_project
- *   workspace NULL, or at least engram_project_mx4_workspace_size bytes, 256-byte
- *             aligned; contents are scratch
+ *   workspace as for engram_project, sized by engram_project_mx4_workspace_size (no
+ *             schedule splits K over blocks today, so that is 0 for every shape)
+ * Each output sums its K in an order that depends on the shape and the CU count only.
  * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
  */
 int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_format,
@@ -772,8 +773,7 @@ int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_form
                        int64_t in_dim, int64_t out_dim, void *workspace,
                        size_t workspace_bytes, hipStream_t stream);
 
-/* [host] Bytes of workspace engram_project_mx4 uses (0 if none, on bad arguments or
- * on a HIP error). */
+/* [host] Bytes of workspace engram_project_mx4 uses (0: none, or bad arguments). */
 size_t engram_project_mx4_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim,
                                          int32_t e_format);
 

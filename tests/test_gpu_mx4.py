@@ -212,7 +212,9 @@ def check_project(tokens, K, N, fmt, workspace=True):
 SHAPES = [(1, 128, 8), (1, 6144, 520), (2, 256, 40), (7, 384, 24), (31, 640, 264), (32, 128, 256),
           (33, 1152, 136), (64, 256, 512), (65, 2176, 72), (100, 384, 1000), (128, 512, 128),
           (129, 640, 392), (255, 1024, 520), (256, 6144, 1032), (257, 256, 264), (300, 384, 776),
-          (513, 1280, 2056), (1003, 896, 520), (1, 20480, 32), (2500, 128, 264), (40, 256, 12808)]
+          (513, 1280, 2056), (1003, 896, 520), (1, 20480, 32), (2500, 128, 264), (40, 256, 12808),
+          (20, 1664, 16392), (100, 1920, 16400), (200, 1408, 16648), (2100, 128, 4104), (2049, 384, 4360),
+          (2305, 1152, 4104), (2111, 1280, 4128)]
 
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
@@ -231,7 +233,7 @@ def test_project_without_a_workspace(fmt, tokens, K, N):
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
 @pytest.mark.parametrize("tokens,K,N", [(3, 384, 40), (70, 640, 136), (256, 1152, 520), (700, 512, 1288),
-                                        (5000, 256, 3336)])
+                                        (5000, 256, 3336), (2100, 640, 4104), (2305, 2176, 4360), (250, 4992, 16392)])
 def test_project_integers_are_exact(fmt, tokens, K, N):
     """Codes of halves and integers at scale 1: every partial sum is a multiple of 1/4
     below 2^16, so fp32 holds it and only the bf16 rounding remains."""
@@ -244,7 +246,8 @@ def test_project_integers_are_exact(fmt, tokens, K, N):
 
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
-@pytest.mark.parametrize("tokens,K,N", [(4, 384, 40), (200, 640, 264), (600, 1152, 1032)])
+@pytest.mark.parametrize("tokens,K,N", [(4, 384, 40), (200, 640, 264), (600, 1152, 1032),
+                                        (2100, 1408, 4104)])
 def test_project_each_input_meets_its_own_weight(fmt, tokens, K, N):
     """e has one nonzero input per token, at its own scale: kv is one exact product."""
     say("project: one input per token", fmt, tokens, K, N)
@@ -264,7 +267,8 @@ def test_project_each_input_meets_its_own_weight(fmt, tokens, K, N):
 
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
-@pytest.mark.parametrize("tokens,K,N", [(3, 384, 40), (130, 384, 264), (700, 640, 520)])
+@pytest.mark.parametrize("tokens,K,N", [(3, 384, 40), (130, 384, 264), (700, 640, 520),
+                                        (2100, 640, 4104), (90, 896, 16392)])
 def test_project_nan_scales_stay_in_their_row(fmt, tokens, K, N):
     """A NaN block scale makes its own row's outputs NaN and no other's; the last block of
     a row lies next to the following row's first in memory."""
