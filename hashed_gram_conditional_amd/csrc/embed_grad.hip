@@ -530,7 +530,7 @@ struct Cols;
 template <bool F32>
 struct Cols<F32, 8> {
   engram::Chunk8<F32> v;
-  __device__ __forceinline__ void load(const void *p, int64_t off) { v.load(p, off / 8); }
+  __device__ __forceinline__ void load(const void *p, int64_t off) { v.load_nt(p, off / 8); }
   __device__ __forceinline__ float operator[](int e) const { return v[e]; }
 };
 template <bool F32>

@@ -12,16 +12,15 @@
 //
 // One pass, bound by HBM: a thread owns 8 values (16 or 32 bytes in, 4 bytes of
 // codes out), four neighbouring threads a block, which exchange their maxima
-// within the quad; 64 threads read 1 or 2 KB in a row. Large calls give a thread two
-// groups in flight; below that the launch and the latency of one load count.
+// within the quad; 64 threads read 1 or 2 KB in a row. One group a thread: two in
+// flight took 254 us for 237 at 25600 x 6144 fp32 with values (1.34 GB, 5.7 TB/s), and
+// 8.4 for 5.9 at 4093 x 1001 bf16.
 #include "common.h"
 #include "fast_div.h"
 
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;
-constexpr int64_t kSmallGroups = (int64_t)1 << 20;      // one group a thread up to here
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -67,6 +66,9 @@ __device__ __forceinline__ void store8(void *dst, int64_t row_off, int64_t col, 
                                        const float (&f)[8]) {
   if (VEC && col + 8 <= cols) {
     engram::Chunk8<F32>::store(dst, (row_off + col) / 8, f);
+    // keeps the compiler from merging these with the single stores below (267 us
+    // for 237 at 25600 x 6144)
+    asm volatile("" ::: "memory");
     return;
   }
 #pragma unroll
@@ -83,67 +85,55 @@ __device__ __forceinline__ void store8(void *dst, int64_t row_off, int64_t col, 
 
 // src and values may be the same buffer (each value is read and written by one
 // thread), so neither is marked restrict.
-template <bool F32, bool VEC, int U>
+template <bool F32, bool VEC>
 __global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(
     const void *src, int64_t cols, int64_t ld, uint32_t *__restrict__ codes,
     uint8_t *__restrict__ scales, void *values, EngramFastDiv groups, int64_t total) {
-  constexpr int64_t kTile = (int64_t)kThreads * U;
-  for (int64_t g0 = (int64_t)blockIdx.x * kTile + threadIdx.x; g0 < total;
-       g0 += (int64_t)gridDim.x * kTile) {
-    uint32_t bits[U][8];
-    int64_t row[U], col[U];
+  for (int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x; g < total;
+       g += (int64_t)gridDim.x * kThreads) {
+    // A quad of threads is one block of 32: total is a multiple of 4, so the four are
+    // in or out of range together.
+    const int64_t row = groups.div(g);
+    const int64_t col = (g - row * groups.d) * 8;
+    uint32_t bits[8], top = 0;
+    load8<F32, VEC>(src, row * ld, col, cols, bits);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t g = g0 + u * kThreads;
-      row[u] = groups.div(g);
-      col[u] = (g - row[u] * groups.d) * 8;
-      if (g < total) load8<F32, VEC>(src, row[u] * ld, col[u], cols, bits[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t g = g0 + u * kThreads;
-      // A quad of threads is one block of 32: total is a multiple of 4, so the
-      // four are in or out of range together.
-      if (g >= total) continue;
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = max(top, bits[u][e] & 0x7FFFFFFFu);
-      top = quad_max<kSwapHalves>(quad_max<kSwapPairs>(top));
-      const uint32_t field = top >> 23;
-      const bool finite = field < 255u;
-      const uint32_t s = finite ? (field > 2u ? field - 2u : 0u) : 255u;
-      // 2^(s - 127); 2^-127 is a subnormal fp32
-      const float scale = __uint_as_float(s > 0u ? s << 23 : 0x00400000u);
-      uint32_t word = 0;
-      if (finite) {
+    for (int e = 0; e < 8; ++e) top = max(top, bits[e] & 0x7FFFFFFFu);
+    top = quad_max<kSwapHalves>(quad_max<kSwapPairs>(top));
+    const uint32_t field = top >> 23;
+    const bool finite = field < 255u;
+    const uint32_t s = finite ? (field > 2u ? field - 2u : 0u) : 255u;
+    // 2^(s - 127); 2^-127 is a subnormal fp32
+    const float scale = __uint_as_float(s > 0u ? s << 23 : 0x00400000u);
+    uint32_t word = 0;
+    if (finite) {
 #define ENGRAM_CVT_FP4(i)                                                                       \
-  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, __uint_as_float(bits[u][2 * (i)]),      \
-                                                  __uint_as_float(bits[u][2 * (i) + 1]), scale, i);
-        ENGRAM_CVT_FP4(0)
-        ENGRAM_CVT_FP4(1)
-        ENGRAM_CVT_FP4(2)
-        ENGRAM_CVT_FP4(3)
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, __uint_as_float(bits[2 * (i)]),         \
+                                                  __uint_as_float(bits[2 * (i) + 1]), scale, i);
+      ENGRAM_CVT_FP4(0)
+      ENGRAM_CVT_FP4(1)
+      ENGRAM_CVT_FP4(2)
+      ENGRAM_CVT_FP4(3)
 #undef ENGRAM_CVT_FP4
-      }
-      codes[g] = word;
-      if ((g & 3) == 0) scales[g >> 2] = (uint8_t)s;
-      if (values != nullptr) {
-        // the codes times the scale, exact; NaN in a marked block
-        const float by = finite ? scale : __uint_as_float(0x7FC00000u);
-        float f[8];
+    }
+    codes[g] = word;
+    if ((g & 3) == 0) scales[g >> 2] = (uint8_t)s;
+    if (values != nullptr) {
+      // the codes times the scale, exact; NaN in a marked block
+      const float by = finite ? scale : __uint_as_float(0x7FC00000u);
+      float f[8];
 #define ENGRAM_FP4_VALUES(i)                                                                    \
   {                                                                                             \
     const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.f, i);                      \
     f[2 * (i)] = v[0] * by;                                                                     \
     f[2 * (i) + 1] = v[1] * by;                                                                 \
   }
-        ENGRAM_FP4_VALUES(0)
-        ENGRAM_FP4_VALUES(1)
-        ENGRAM_FP4_VALUES(2)
-        ENGRAM_FP4_VALUES(3)
+      ENGRAM_FP4_VALUES(0)
+      ENGRAM_FP4_VALUES(1)
+      ENGRAM_FP4_VALUES(2)
+      ENGRAM_FP4_VALUES(3)
 #undef ENGRAM_FP4_VALUES
-        store8<F32, VEC>(values, row[u] * ld, col[u], cols, f);
-      }
+      store8<F32, VEC>(values, row * ld, col, cols, f);
     }
   }
 }
@@ -156,22 +146,18 @@ hipError_t engram_launch_quantize_mx4(bool f32, const void *src, int64_t rows, i
   if (rows <= 0 || out_cols <= 0) return hipSuccess;
   const EngramFastDiv groups(out_cols / 8);
   const int64_t total = rows * groups.d;
-  const int unroll = total <= kSmallGroups ? 1 : kUnroll;
-  const int64_t tiles = (total + kThreads * unroll - 1) / (kThreads * unroll);
+  const int64_t tiles = (total + kThreads - 1) / kThreads;
   const int64_t limit = (int64_t)1 << 22;
   const dim3 grid((unsigned)(tiles < limit ? tiles : limit));
   uint32_t *words = reinterpret_cast<uint32_t *>(codes);
   const bool vec = ld % 8 == 0;
-#define ENGRAM_QUANTIZE(F, V, U)                                                                \
-  hipLaunchKernelGGL((quantize_mx4_kernel<F, V, U>), grid, dim3(kThreads), 0, stream, src, cols, \
-                     ld, words, scales, values, groups, total)
-#define ENGRAM_QUANTIZE_BY_SIZE(F, V) \
-  { if (unroll == 1) ENGRAM_QUANTIZE(F, V, 1); else ENGRAM_QUANTIZE(F, V, kUnroll); }
-  if (f32 && vec) ENGRAM_QUANTIZE_BY_SIZE(true, true)
-  else if (f32) ENGRAM_QUANTIZE_BY_SIZE(true, false)
-  else if (vec) ENGRAM_QUANTIZE_BY_SIZE(false, true)
-  else ENGRAM_QUANTIZE_BY_SIZE(false, false)
-#undef ENGRAM_QUANTIZE_BY_SIZE
+#define ENGRAM_QUANTIZE(F, V)                                                                   \
+  hipLaunchKernelGGL((quantize_mx4_kernel<F, V>), grid, dim3(kThreads), 0, stream, src, cols, ld, \
+                     words, scales, values, groups, total)
+  if (f32 && vec) ENGRAM_QUANTIZE(true, true);
+  else if (f32) ENGRAM_QUANTIZE(true, false);
+  else if (vec) ENGRAM_QUANTIZE(false, true);
+  else ENGRAM_QUANTIZE(false, false);
 #undef ENGRAM_QUANTIZE
   return hipGetLastError();
 }
