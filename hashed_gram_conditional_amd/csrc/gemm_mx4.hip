@@ -151,6 +151,13 @@ __global__ __launch_bounds__(kThinWaves * 64) void mx4_thin_kernel(Mx4Operands o
 // sits in slot c ^ f(row), so the 8 rows a quarter-wave reads fall into 8 different
 // slots of 128 bytes. Scales come for two K-steps at once (16 or 8 bytes of a row, half
 // as many cache lines as one step at a time) and are kept in registers.
+//
+// One block per CU walks the tiles: the loads of the two steps behind a tile's last
+// are the next tile's first two, so they are in flight while the finished tile is
+// stored, and the stores while the next one begins (32768 x 1024 x 25600: 655 -> 560 us,
+// with 6144 inputs 2.57 -> 2.55 ms: there power sets the clock, 1.76 GHz with the matrix
+// units 54 % busy; an MFMA loop of nothing else reaches 6.4 PFLOP/s, with the LDS reads
+// 6.0, this kernel 4.0).
 template <int EF>
 struct WideCfg {
   static constexpr int kStep = EF == kFp4 ? 256 : 128;      // inputs of a K-step
@@ -160,43 +167,68 @@ struct WideCfg {
   static constexpr int kSc = kStep / 32;                    // scale bytes of a row
 };
 
-// The stages are separate LDS variables: the compiler then knows that direct loads
-// into one and reads of another do not meet, and waits for nothing in between.
-#define ENGRAM_MX4_WIDE_LDS(EF)                                                                \
-  __shared__ __align__(1024) uint8_t w0[BN * WideCfg<EF>::kWRow];                              \
-  __shared__ __align__(1024) uint8_t w1[BN * WideCfg<EF>::kWRow];                              \
-  __shared__ __align__(1024) uint8_t e0[BM * WideCfg<EF>::kERow];                              \
-  __shared__ __align__(1024) uint8_t e1[BM * WideCfg<EF>::kERow];                              \
-  __shared__ __align__(1024) uint8_t sc[(BN + BM) * 2 * WideCfg<EF>::kSc] /* W rows, then e rows */
+constexpr int kPatch = 4096;          // LDS of a wave for storing 32 tokens x 64 columns
 
-// K-steps [ks, ke) of the tile at (m0, n0) into acc (zeroed by the caller).
+// Stores 32 tokens (j) x 64 columns (accumulators i, i + 1) of a wave in whole cache
+// lines. A lane's accumulators are 4 columns of one token at a time, 16 bytes of a
+// line with its partner's: stored from the registers, a tile's 128 KB took 4 times as
+// many write transactions as lines. So they pass through LDS (chunk c of token t in
+// slot c ^ t % 8), and 8 lanes store 128 bytes of a token. The stores are marked
+// nontemporal, so that kv does not push the operands' panels out of L2 (2.83 -> 2.57
+// ms at 32768 x 6144 x 25600). GUARD: the tile passes the end of kv.
+template <bool GUARD>
+__device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, uint8_t *patch,
+                                            uint16_t *__restrict__ kv, int M, int N, int m, int n,
+                                            int lane) {
+  const int frow = lane & 31, fk = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x16 &a = i ? a1 : a0;
+      uint2 v;
+      v.x = engram::pack_bf16x2(a[g * 4 + 0], a[g * 4 + 1]);
+      v.y = engram::pack_bf16x2(a[g * 4 + 2], a[g * 4 + 3]);
+      *reinterpret_cast<uint2 *>(patch + frow * 128 + (((i * 4 + g) ^ (frow & 7)) << 4) + fk * 8) = v;
+    }
+  const int col = n + (lane & 7) * 8;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int t = q * 8 + (lane >> 3);
+    const engram::u32x4 v =
+        *reinterpret_cast<const engram::u32x4 *>(patch + t * 128 + (((lane & 7) ^ (t & 7)) << 4));
+    if (!GUARD || (m + t < M && col < N))
+      __builtin_nontemporal_store(v, reinterpret_cast<engram::u32x4 *>(kv + (int64_t)(m + t) * N + col));
+  }
+}
+constexpr int kTileStores = 32;       // store instructions of a wave and tile
+
+// The tiles blockIdx.x, blockIdx.x + gridDim.x, ... of tiles_m x tiles_n. With an odd
+// number of K-steps each block has one tile (the stages would change places).
 template <int EF>
-__device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int n0, int ks, int ke,
-                                              f32x16 (&acc)[4][4], uint8_t *__restrict__ w0,
-                                              uint8_t *__restrict__ w1, uint8_t *__restrict__ e0,
-                                              uint8_t *__restrict__ e1, uint8_t *__restrict__ sc) {
+__device__ __forceinline__ void wide_walk(const Mx4Operands &op, uint16_t *__restrict__ kv, int tiles_m,
+                                          int tiles_n) {
   using Cfg = WideCfg<EF>;
   constexpr int kSub = Cfg::kSub, kWRow = Cfg::kWRow, kSc = Cfg::kSc;
   constexpr int kWLoads = BN * kWRow / 1024 / 4;            // direct loads of a wave and step
   constexpr int kSLoads = (BN + BM) * 2 * kSc / 256 / 4;    // of a wave and two steps
   constexpr int kReads = EF == kFp4 ? 8 : 12;               // LDS reads of one set of fragments
+  constexpr int kScBytes = (BN + BM) * 2 * kSc;
+  // The stages are separate LDS variables: the compiler then knows that direct loads
+  // into one and reads of another do not meet, and waits for nothing in between. (The
+  // patches share the scales' variable: reads of one that no load meets would wait for
+  // all of them.)
+  __shared__ __align__(1024) uint8_t w0[BN * kWRow], w1[BN * kWRow];
+  __shared__ __align__(1024) uint8_t e0[BM * Cfg::kERow], e1[BM * Cfg::kERow];
+  __shared__ __align__(1024) uint8_t sc[kScBytes + 4 * kPatch];   // W rows, e rows; patches
+  const int tiles = tiles_m * tiles_n;
+  const int ke = (op.K + Cfg::kStep - 1) / Cfg::kStep;
   const int KB = op.K / 32;
   const int w_ld = op.K / 2, e_ld = EF == kFp4 ? op.K / 2 : op.K;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave >> 1, wm = wave & 1;
-  const int rows_w = min(BN, op.N - n0), rows_e = min(BM, op.M - m0);
-  const __amdgpu_buffer_rsrc_t rsW = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(op.w_codes + (int64_t)n0 * w_ld), 0, rows_w * w_ld, kBufferFlags);
-  const __amdgpu_buffer_rsrc_t rsE = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(op.e_codes + (int64_t)m0 * e_ld), 0, rows_e * e_ld, kBufferFlags);
-  // waves 0 and 1 load W's scales, 2 and 3 e's
-  const __amdgpu_buffer_rsrc_t rsS =
-      wave < 2 ? __builtin_amdgcn_make_buffer_rsrc(
-                     const_cast<uint8_t *>(op.w_scales + (int64_t)n0 * KB), 0, rows_w * KB, kBufferFlags)
-               : __builtin_amdgcn_make_buffer_rsrc(
-                     const_cast<uint8_t *>(op.e_scales + (int64_t)m0 * KB), 0, rows_e * KB, kBufferFlags);
   // Direct load i of a wave fills 1 KB: 8 rows of 128 bytes (lane p: row p / 8, slot
   // p % 8) or 16 rows of 64 (row p / 4, slot p % 4).
   const int dl_c = (lane & 7) ^ (lane >> 3);
@@ -217,6 +249,28 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
   const int as_base = (wn * 128 + frow) * 2 * kSc + h * (kSc / 2);
   const int bs_base = (BN + wm * 128 + frow) * 2 * kSc + h * (kSc / 2);
 
+  // The operands of tile t_, from which the loads come; behind the last tile nothing
+  // does. Waves 0 and 1 load W's scales, 2 and 3 e's.
+  __amdgpu_buffer_rsrc_t rsW, rsE, rsS;
+#define M4_AIM(t_)                                                                             \
+  {                                                                                            \
+    const int at_ = (t_);                                                                      \
+    int am_ = 0, an_ = 0;                                                                      \
+    if (at_ < tiles) tile_origin_of(at_, tiles_m, tiles_n, BN, am_, an_);                      \
+    const int rw_ = at_ < tiles ? min(BN, op.N - an_) : 0;                                     \
+    const int re_ = at_ < tiles ? min(BM, op.M - am_) : 0;                                     \
+    rsW = __builtin_amdgcn_make_buffer_rsrc(                                                   \
+        const_cast<uint8_t *>(op.w_codes + (int64_t)an_ * w_ld), 0, rw_ * w_ld, kBufferFlags); \
+    rsE = __builtin_amdgcn_make_buffer_rsrc(                                                   \
+        const_cast<uint8_t *>(op.e_codes + (int64_t)am_ * e_ld), 0, re_ * e_ld, kBufferFlags); \
+    rsS = wave < 2 ? __builtin_amdgcn_make_buffer_rsrc(                                        \
+                         const_cast<uint8_t *>(op.w_scales + (int64_t)an_ * KB), 0, rw_ * KB,  \
+                         kBufferFlags)                                                         \
+                   : __builtin_amdgcn_make_buffer_rsrc(                                        \
+                         const_cast<uint8_t *>(op.e_scales + (int64_t)am_ * KB), 0, re_ * KB,  \
+                         kBufferFlags);                                                        \
+  }
+
 #define M4_W(st) ((st) ? w1 : w0)
 #define M4_E(st) ((st) ? e1 : e0)
 #define M4_LDS(p) ((__attribute__((address_space(3))) void *)(p))
@@ -228,7 +282,7 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rsE, M4_LDS(&M4_E(st)[(wave * 8 + (i)) * 1024]), 16, \
                                            ((i) & 1) ? e_v1 : e_v0,                            \
                                            (i) * 8 * e_ld + (kt_) * Cfg::kERow, 0, 0);
-// the scales of steps kt_ and kt_ + 1 (kt_ - ks even)
+// the scales of steps kt_ and kt_ + 1 (kt_ even)
 #define M4_LOADS(kt_)                                                                          \
   _Pragma("unroll") for (int i = 0; i < kSLoads; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
       rsS, M4_LDS(&sc[(wave * kSLoads + i) * 256]), 4, s_v, i * kSRows * KB + (kt_) * kSc, 0, 0);
@@ -255,7 +309,14 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 #define M4_MFMA(s, fa, fb, sA, sB)                                                             \
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = mfma_unit<EF, s>(fa[i], fb[j], acc[i][j], sA[i], sB[j]);
-#define M4_BARRIER() asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory")
+#define M4_BARRIER() asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// the first step of a tile: the stores of the one before may be outstanding, all of
+// them, as they were issued behind the loads
+#define M4_BARRIER0()                                                                          \
+  if (stores)                                                                                  \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kTileStores) : "memory"); \
+  else                                                                                         \
+    M4_BARRIER()
 // E2M1, in_dim an odd multiple of 128: the last step's upper four blocks lie in the
 // next row. Scales of 2^-127 on both sides take their products below the smallest
 // fp32, to zero.
@@ -265,18 +326,17 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
     _Pragma("unroll") for (int i = 0; i < 4; ++i) { sA[i] &= keep; sB[i] &= keep; }            \
   }
 
+  f32x16 acc[4][4];
   i32x8 fa0[4], fb0[4], fa1[4], fb1[4];
   uint32_t sA0[4], sB0[4], sA1[4], sB1[4];
-  __syncthreads();
-  M4_LOADS(ks)
-  M4_LOADSTEP(ks, 0)
-  M4_LOADSTEP(ks + 1, 1)
-  M4_BARRIER();
-  M4_FRAGS(0, 0, fa0, fb0)
-  M4_SCALES(0, sA0, sB0)
-  M4_SCALES(1, sA1, sB1)
+  zero_acc(acc);
+  M4_AIM((int)blockIdx.x)
+  M4_LOADS(0)
+  M4_LOADSTEP(0, 0)
+  M4_LOADSTEP(1, 1)
+  M4_BARRIER()
 // One step from stage P: its last fragments are read before the barrier, the next
-// step's first ones (stage Q) behind it, while stage P takes step kt + 2. The LDS
+// step's first ones (stage Q) behind it, while stage P takes step `ahead`. The LDS
 // reads come before the new direct loads: the compiler, which cannot see the wait
 // inside the barrier, puts a full vmcnt wait before them.
 #define M4_FENCE() __builtin_amdgcn_sched_barrier(0)
@@ -287,7 +347,7 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
   M4_MFMA(s, fa, fb, sA, sB)                                                                   \
   _Pragma("unroll") for (int g_ = 0; g_ < kReads; ++g_) { M4_GROUP(0x100, 1); M4_GROUP(0x008, 1); } \
   M4_FENCE();
-#define M4_STEP(kt_, P, Q, sA, sB, READ, LOAD)                                                 \
+#define M4_STEP(kt_, ahead, P, Q, sA, sB, BARRIER, READ, LOAD)                                 \
   {                                                                                            \
     M4_TAIL(kt_, sA, sB)                                                                       \
     if constexpr (kSub == 4) {                                                                 \
@@ -297,11 +357,11 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
     } else {                                                                                   \
       M4_PART(P, 0, fa1, fb1, fa0, fb0, sA, sB)                                                \
     }                                                                                          \
-    M4_BARRIER();                                                                              \
+    BARRIER                                                                                    \
     M4_FENCE();                                                                                \
     M4_FRAGS(Q, 0, fa0, fb0)                                                                   \
     READ                                                                                       \
-    M4_LOADSTEP((kt_) + 2, P)                                                                  \
+    M4_LOADSTEP(ahead, P)                                                                      \
     LOAD                                                                                       \
     M4_MFMA((kSub - 1), fa1, fb1, sA, sB)                                                      \
     _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                        \
@@ -309,25 +369,59 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
     }                                                                                          \
     M4_FENCE();                                                                                \
   }
-  int kt = ks;
-  for (; kt + 1 < ke; kt += 2) {
-    M4_STEP(kt, 0, 1, sA0, sB0, , M4_LOADS(kt + 2))
-    uint32_t tA[4], tB[4];
-    M4_STEP(kt + 1, 1, 0, sA1, sB1, M4_SCALES(0, sA0, sB0) M4_SCALES(1, tA, tB), )
+  bool stores = false;                // a whole tile's stores were issued behind the loads
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    // read again behind the stores, whose registers they would otherwise take
+    M4_FRAGS(0, 0, fa0, fb0)
+    M4_SCALES(0, sA0, sB0)
+    M4_SCALES(1, sA1, sB1)
+    int kt = 0;
+    for (; kt + 1 < ke; kt += 2) {
+      int ahead = kt + 2;
+      if (ahead >= ke) {              // the next tile's first steps
+        M4_AIM(t + (int)gridDim.x)
+        ahead = 0;
+      }
+      M4_STEP(kt, ahead, 0, 1, sA0, sB0, M4_BARRIER0(), , M4_LOADS(ahead))
+      stores = false;
+      uint32_t tA[4], tB[4];
+      M4_STEP(kt + 1, ahead + 1, 1, 0, sA1, sB1, M4_BARRIER(), M4_SCALES(0, sA0, sB0) M4_SCALES(1, tA, tB), )
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sA1[i] = tA[i];
-      sB1[i] = tB[i];
+      for (int i = 0; i < 4; ++i) {
+        sA1[i] = tA[i];
+        sB1[i] = tB[i];
+      }
     }
+    if (kt < ke) M4_STEP(kt, kt + 2, 0, 1, sA0, sB0, M4_BARRIER(), , )
+    int m0, n0;
+    tile_origin_of(t, tiles_m, tiles_n, BN, m0, n0);
+    uint8_t *patch = sc + kScBytes + wave * kPatch;
+    const bool whole = m0 + BM <= op.M && n0 + BN <= op.N;
+    // the lane through a swap with itself, which stays in the loop: addresses formed
+    // from it are formed anew for each tile; kept over the K loop they spill
+    const int l = __builtin_amdgcn_mov_dpp(lane, 0xE4, 0xF, 0xF, true);
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        store_patch<false>(acc[q % 2 * 2][q / 2], acc[q % 2 * 2 + 1][q / 2], patch, kv, op.M, op.N,
+                           m0 + wm * 128 + q / 2 * 32, n0 + wn * 128 + q % 2 * 64, l);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        store_patch<true>(acc[q % 2 * 2][q / 2], acc[q % 2 * 2 + 1][q / 2], patch, kv, op.M, op.N,
+                          m0 + wm * 128 + q / 2 * 32, n0 + wn * 128 + q % 2 * 64, l);
+    }
+    zero_acc(acc);
+    stores = whole;
   }
-  if (kt < ke) M4_STEP(kt, 0, 1, sA0, sB0, , )
-  // direct loads issued for steps past ke land before the stages are reused
+  // direct loads issued behind the last tile land before the block's LDS is freed
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #undef M4_STEP
 #undef M4_PART
 #undef M4_GROUP
 #undef M4_FENCE
 #undef M4_TAIL
+#undef M4_BARRIER0
 #undef M4_BARRIER
 #undef M4_MFMA
 #undef M4_SCALES
@@ -341,57 +435,13 @@ __device__ __forceinline__ void wide_tile_mx4(const Mx4Operands &op, int m0, int
 #undef M4_LDS
 #undef M4_E
 #undef M4_W
-}
-
-// bf16 store of a finished tile in whole cache lines. A lane's accumulators are 4
-// columns of one token at a time, 16 bytes of a line with its partner's: stored from
-// the registers, a tile's 128 KB took 4 times as many write transactions as lines.
-// Each wave passes 32 tokens x 128 columns at a time through 8 KB of LDS (chunk c of
-// token t in slot c ^ t % 16) and stores 256 bytes of a token with 16 lanes. The
-// stores are marked nontemporal, so that kv does not push the operands' panels out of
-// L2 (2.83 -> 2.57 ms at 32768 x 6144 x 25600).
-__device__ __forceinline__ void wide_store_lines(const f32x16 (&acc)[4][4], uint16_t *__restrict__ kv,
-                                                 int M, int N, int m0, int n0, uint8_t *buf) {
-  const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int wn = wave >> 1, wm = wave & 1;
-  const int frow = lane & 31, fk = lane >> 5;
-  uint8_t *mine = buf + wave * 8192;
-  const int col = n0 + wn * 128 + (lane & 15) * 8;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        uint2 v;
-        v.x = engram::pack_bf16x2(acc[i][j][g * 4 + 0], acc[i][j][g * 4 + 1]);
-        v.y = engram::pack_bf16x2(acc[i][j][g * 4 + 2], acc[i][j][g * 4 + 3]);
-        *reinterpret_cast<uint2 *>(mine + frow * 256 + (((i * 4 + g) ^ (frow & 15)) << 4) + fk * 8) = v;
-      }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int t = q * 4 + (lane >> 4);
-      const engram::u32x4 v = *reinterpret_cast<const engram::u32x4 *>(mine + t * 256 + (((lane & 15) ^ (t & 15)) << 4));
-      const int m = m0 + wm * 128 + j * 32 + t;
-      if (m < M && col < N)
-        __builtin_nontemporal_store(v, reinterpret_cast<engram::u32x4 *>(kv + (int64_t)m * N + col));
-    }
-  }
+#undef M4_AIM
 }
 
 template <int EF>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int tiles_n) {
-  ENGRAM_MX4_WIDE_LDS(EF);
-  int m0, n0;
-  tile_origin(tiles_m, tiles_n, BN, m0, n0);
-  f32x16 acc[4][4];
-  zero_acc(acc);
-  wide_tile_mx4<EF>(op, m0, n0, 0, (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep, acc, w0,
-                    w1, e0, e1, sc);
-  __syncthreads();                    // every wave is done with the stages
-  wide_store_lines(acc, kv, op.M, op.N, m0, n0, e0);
+  wide_walk<EF>(op, kv, tiles_m, tiles_n);
 }
 
 // ---- up to 256 tokens: columns dealt to every CU, the weight streamed far ahead ------
@@ -634,8 +684,10 @@ hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
     return narrow ? launch_skinny<EF, 2, 2>(op, kv, stream) : launch_skinny<EF, 4, 2>(op, kv, stream);
   }
   const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
-  hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(tiles_m * tiles_n)), dim3(kWideThreads), 0,
-                     stream, op, kv, tiles_m, tiles_n);
+  const int tiles = tiles_m * tiles_n;
+  const bool even = (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep % 2 == 0;
+  hipLaunchKernelGGL((mx4_wide_kernel<EF>), dim3((unsigned)(even && tiles > cus ? cus : tiles)),
+                     dim3(kWideThreads), 0, stream, op, kv, tiles_m, tiles_n);
   return hipGetLastError();
 }
 

@@ -20,11 +20,11 @@ constexpr int kXcds = 8;
 // Buffer resource word 3 for gfx9-family raw buffers (no format, no swizzle).
 constexpr int kBufferFlags = 0x00020000;
 
-// Tile origin of this block: block ids are renumbered so that each XCD's
+// Origin of tile bid (block bid's): block ids are renumbered so that each XCD's
 // blocks are contiguous, then walked in groups of kGroupM token-tiles.
-__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bn, int &m0, int &n0) {
+__device__ __forceinline__ void tile_origin_of(int bid, int tiles_m, int tiles_n, int bn, int &m0,
+                                               int &n0) {
   const int nblocks = tiles_m * tiles_n;
-  int bid = blockIdx.x;
   const int full = (nblocks / kXcds) * kXcds;
   if (bid < full) bid = (bid % kXcds) * (full / kXcds) + bid / kXcds;
   const int in_group = kGroupM * tiles_n;
@@ -34,6 +34,10 @@ __device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bn, in
   const int local = bid - group * in_group;
   m0 = (first_m + local % gsize) * BM;
   n0 = (local / gsize) * bn;
+}
+
+__device__ __forceinline__ void tile_origin(int tiles_m, int tiles_n, int bn, int &m0, int &n0) {
+  tile_origin_of(blockIdx.x, tiles_m, tiles_n, bn, m0, n0);
 }
 
 __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t rs, int voff, int soff) {
