@@ -173,10 +173,6 @@ __device__ __forceinline__ void zero_grad(const Sums &s, const Zero &z, int64_t 
   }
 }
 
-__global__ __launch_bounds__(256) void zero_grad_kernel(Sums s, Zero z) {
-  zero_grad(s, z, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
-}
-
 // ---- the sort of up to kSmall ids -------------------------------------------------
 // The first blocks of a launch do its work; the others (a dense gradient that is not
 // added to) clear their share of the gradient meanwhile.
@@ -281,8 +277,9 @@ __device__ __forceinline__ uint2 sort_pair(const int64_t *ids, const uint2 *pair
 template <bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(
     const int64_t *__restrict__ ids, const uint2 *__restrict__ pairs, int64_t table_rows, Pass a,
-    uint32_t *__restrict__ counts) {
+    uint32_t *__restrict__ counts, Sums s, Zero z) {
   __shared__ uint32_t hist[1 << kMaxBits];
+  if (zero_block<kSortThreads>(s, z, a.blocks)) return;
   const int digits = 1 << a.bits;
   for (int d = threadIdx.x; d < digits; d += kSortThreads) hist[d] = 0u;
   __syncthreads();
@@ -877,9 +874,7 @@ hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
     hipLaunchKernelGGL(small_runs_kernel, dim3((unsigned)tiles + zero_blocks(kSmallTile)),
                        dim3(kSmallTile), 0, stream, (int)p.n, a.table_rows, r, tiles, s, z);
   } else {
-    z.end = zero_total;
-    if (z.end > 0)
-      hipLaunchKernelGGL(zero_grad_kernel, dim3(zero_blocks(256)), dim3(256), 0, stream, s, z);
+    z.end = zero_total;               // cleared beside the first count
     Pass pass = p.pass;
     int at = 1;                       // the next pass writes pairs[1 - at]
     for (int i = 0; i < p.passes; ++i) {
@@ -888,11 +883,11 @@ hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
       const dim3 grid((unsigned)pass.blocks), block(kSortThreads);
       const uint2 *from = pairs[at];
       if (i == 0)
-        hipLaunchKernelGGL(sort_count_kernel<true>, grid, block, 0, stream, row_ids, from, a.table_rows,
-                           pass, counts);
+        hipLaunchKernelGGL(sort_count_kernel<true>, dim3((unsigned)pass.blocks + zero_blocks(kSortThreads)),
+                           block, 0, stream, row_ids, from, a.table_rows, pass, counts, s, z);
       else
         hipLaunchKernelGGL(sort_count_kernel<false>, grid, block, 0, stream, row_ids, from, a.table_rows,
-                           pass, counts);
+                           pass, counts, s, z);
       hipLaunchKernelGGL(sort_scan_kernel, dim3(((1u << p.digit) + kScanDigits - 1) / kScanDigits),
                          dim3(kScanThreads), 0, stream, counts, totals, pass.blocks, 1 << p.digit);
       if (i == 0)
