@@ -8,7 +8,8 @@
 // row l % 32. Its 16 bytes of E2M1 are inputs [32 h, 32 h + 32) of the 64 in order;
 // its 32 bytes of E4M3 are inputs [16 h, 16 h + 16) and [32 + 16 h, 48 + 16 h). The
 // scale of inputs [32 h, 32 h + 32) comes from the lanes of half h, from one byte of
-// a register that the instruction selects. That register must be a vector one.
+// a register that the instruction selects. That register must be a vector one: with a
+// constant operand the upper half's blocks lost their scale.
 //
 // A product over the inputs may take them in any order that both operands share.
 // Here half h of a wave takes blocks 4 h .. 4 h + 3 of each 8 blocks (256 inputs),

@@ -1,6 +1,7 @@
 /*
  * engram.h -- C ABI of the Engram conditional-memory layer forward for
- * AMD Instinct MI355X (gfx950).
+ * AMD Instinct MI355X (gfx950), with the scaled lookup of a table and its
+ * gradient, and the 4-bit quantiser and projection.
  *
  * The layer (pages cited by title, then section / equation / table):
  *   [P1] "DeepSeek-V4.1 模型结构（5）：记忆，Engram"
