@@ -621,7 +621,7 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
 #undef MK_LDS
 #undef MK_E
 #undef MK_W
-  // 32 tokens x 32 NI columns of a wave at a time through LDS, as wide_store_lines
+  // 32 tokens x 32 NI columns of a wave at a time through LDS, as store_patch
   constexpr int kChunks = 4 * NI;                       // 16-byte chunks of a token
   constexpr int kPatch = 32 * kChunks * 16;
   static_assert(EF == kFp4 ? kPatch <= kToks * kERow : 2 * kPatch <= kToks * kERow, "patches fit the e slots");

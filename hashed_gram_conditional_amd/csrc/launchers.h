@@ -126,7 +126,8 @@ hipError_t engram_launch_embed(const EngramEmbedArgs &a, const void *table,
                                hipStream_t stream);
 
 // The table's gradient by sorted ids. n_rows set: the touched rows side by side;
-// NULL: into the dense array grad, overwritten or (accumulate) added to. The workspace holds engram_embed_grad_workspace bytes.
+// NULL: into the dense array grad, overwritten or (accumulate) added to. The workspace
+// holds engram_embed_grad_workspace bytes.
 size_t engram_embed_grad_workspace(const EngramEmbedArgs &a);
 hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
                                     const int64_t *row_ids, float *grad, int64_t *grad_rows,

@@ -680,7 +680,7 @@ int engram_forward_conv(const engram_hash_params *params, const engram_forward_d
  *            rows are not written
  * The product is formed in fp32 and rounded once to out_type (nearest, ties to
  * even). Rows of a multiple of 8 values at strides that are multiples of 8 move
- * in 16-byte accesses, others value by value.
+ * in 16-byte accesses, others value by value. out must not overlap the table.
  * Errors: ENGRAM_EINVAL (also: scale not finite, unknown type), ENGRAM_ESHAPE,
  * ENGRAM_EHIP.
  */

@@ -141,8 +141,8 @@ def _check_sparse(ids, d_out, R, dim, ot, scale, out_ld=0):
     return rows, grad
 
 
-# (n, rows of the table, dim, ids): sizes around the parts of 1024 ids, the merge's
-# limit of 32768 and the large sort's tiles, runs on both sides of 64
+# (n, rows of the table, dim, ids): sizes around the small sort's parts and tiles, the
+# merge's limit of 32768 and the large sort's tiles, runs on both sides of 64
 SPREAD = [
     (1, 5, 8, "uniform"), (2, 1, 3, "uniform"), (63, 7, 256, "uniform"), (64, 1, 8, "uniform"),
     (65, 1, 8, "uniform"), (129, 2, 40, "uniform"), (1000, 100_000, 256, "uniform"),
@@ -328,3 +328,115 @@ def test_a_training_step_of_a_table():
     lim += U32 * (exp.abs() + lim)
     assert ((dev_table.cpu().double() - exp).abs() <= lim).all()
     assert out.shape == (n, dim)
+
+
+# ---- calls at once, replayed, and of the largest sizes ------------------------------
+
+WIDE_LD = (1 << 21) + 8          # 1100 rows at this stride pass 2^31 elements
+
+
+def test_rows_far_apart():
+    """Strides that take the lookup's output, d_out and the dense gradient past 2^31
+    elements give what dense rows give."""
+    say("embed, grad: offsets beyond 2^31 elements")
+    n, R, dim = 1100, 1100, 24
+    ids = _ids(n, R, "uniform", 21).to(DEV)
+    table = _rand((R, dim), 22, torch.bfloat16).to(DEV)
+    near = _embed(table, ids, dim, E.BF16, E.BF16, 0.5)
+    far = torch.zeros((n, WIDE_LD), dtype=torch.bfloat16, device=DEV)
+    E.engram_embed(E.embed_desc(R, n, dim, E.BF16, E.BF16, 0.5, 0, WIDE_LD), table, ids, far)
+    torch.cuda.synchronize()
+    assert torch.equal(far[:, :dim], near)
+    a = _grad(ids, near, R, dim, E.BF16, 0.75)
+    b = _grad(ids, far, R, dim, E.BF16, 0.75, out_ld=WIDE_LD)
+    assert a[2] == b[2] and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c = _grad(ids, near, R, dim, E.BF16, 0.75, dense=(torch.empty((R, dim), device=DEV), 0))
+    for accumulate, start in ((0, 3.0), (1, 0.0)):
+        wide = torch.full((R, WIDE_LD), start, device=DEV)
+        _grad(ids, near, R, dim, E.BF16, 0.75, table_ld=WIDE_LD, dense=(wide, accumulate))
+        assert torch.equal(wide[:, :dim], c) and (wide[:, dim:dim + 64] == start).all()
+        assert (wide[-1, dim:] == start).all()
+        del wide
+
+
+def test_grad_of_the_most_ids():
+    """2^28 ids, of which the first ones name a row twice: every gradient is 1 or 2."""
+    say("grad: 2^28 ids")
+    n, m, step = E.MAX_EMBED_GRAD_IDS, 200_000_003, 21
+    ids = torch.arange(n, device=DEV).remainder_(m).mul_(step)
+    R = m * step                                   # 4.2e9 rows
+    d = E.embed_desc(R, n, 1, E.BF16, E.BF16)
+    size = E.engram_embed_grad_workspace_size(d)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    d_out = torch.ones((n, 1), dtype=torch.bfloat16, device=DEV)
+    rows = torch.empty(n, dtype=torch.int64, device=DEV)
+    grad = torch.full((n, 1), 7.0, device=DEV)
+    count = torch.zeros(1, dtype=torch.int64, device=DEV)
+    E.engram_embed_grad(d, d_out, ids, rows, grad, count, ws, size)
+    torch.cuda.synchronize()
+    assert int(count) == m
+    assert torch.equal(rows[:m], torch.arange(m, device=DEV).mul_(step)) and (rows[m:] == -1).all()
+    assert (grad[:n - m] == 2).all() and (grad[n - m:m] == 1).all() and (grad[m:] == 7).all()
+
+
+@pytest.mark.parametrize("n,R", [(700, 50), (12216, 3000), (60_000, 900)])
+def test_calls_at_once_on_two_streams(n, R):
+    say("grad: two streams at once", n, R)
+    dim = 72
+    cases = []
+    for k in range(2):
+        ids, d_out = _ids(n, R, "zipf", 30 + k), _rand((n, dim), 40 + k, torch.float32)
+        want = _grad(ids, d_out, R, dim, E.F32, 0.5)
+        full = _grad(ids, d_out, R, dim, E.F32, 0.5, dense=(torch.empty((R, dim), device=DEV), 0))
+        cases.append((ids.to(DEV), d_out.to(DEV), want, full))
+    d = E.embed_desc(R, n, dim, E.F32, E.F32, 0.5)
+    size = E.engram_embed_grad_workspace_size(d)
+    bufs = []
+    for k in range(2):
+        bufs.append((torch.empty(size, dtype=torch.uint8, device=DEV),
+                     torch.zeros(n, dtype=torch.int64, device=DEV), torch.zeros((n, dim), device=DEV),
+                     torch.zeros(1, dtype=torch.int64, device=DEV), torch.zeros((R, dim), device=DEV),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (ids, d_out, _, _), (ws, rows, grad, count, full, stream) in zip(cases, bufs):
+            # the two calls of a stream share its workspace
+            E.engram_embed_grad(d, d_out, ids, rows, grad, count, ws, size, stream)
+            E.engram_embed_grad_dense(d, d_out, ids, full, 0, ws, size, stream)
+    torch.cuda.synchronize()
+    for (_, _, (rows0, grad0, count0), full0), (_, rows, grad, count, full, _) in zip(cases, bufs):
+        assert int(count) == count0 and torch.equal(rows.cpu(), rows0)
+        assert torch.equal(grad[:count0].cpu(), grad0[:count0]) and torch.equal(full, full0)
+
+
+@pytest.mark.parametrize("n,R,table_ld", [(900, 300, 0), (900, 300, 76), (40_000, 2000, 0)])
+def test_dense_gradient_in_a_graph(n, R, table_ld):
+    """Captured twice over, written and then added to: every replay, with eager work
+    between, gives the bits of the eager calls."""
+    say("grad dense: replays", n, R, table_ld)
+    dim = 72
+    ids, d_out = _ids(n, R, "zipf", 50).to(DEV), _rand((n, dim), 51, torch.bfloat16).to(DEV)
+    d = E.embed_desc(R, n, dim, E.BF16, E.BF16, 0.5, table_ld)
+    size = E.engram_embed_grad_workspace_size(d)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    grad = torch.full((R, table_ld or dim), 3.0, device=DEV)
+
+    def step():
+        E.engram_embed_grad_dense(d, d_out, ids, grad, 0, ws, size)
+        E.engram_embed_grad_dense(d, d_out, ids, grad, 1, ws, size)
+
+    step()
+    torch.cuda.synchronize()
+    first = grad.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k in range(3):
+        grad[:, :dim] = float(k)
+        ws.fill_(17 * k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, first)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, first)

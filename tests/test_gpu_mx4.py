@@ -146,6 +146,50 @@ def test_quantize_in_place_without_values_and_empty():
     E.engram_quantize_mx4(None, E.F32, 0, 64, 0, 64, None, None, None)
 
 
+@pytest.mark.parametrize("st", [E.BF16, E.F32])
+def test_quantize_rows_far_apart(st):
+    """A stride that takes the rows past 2^31 elements."""
+    say("quantize: offsets beyond 2^31 elements", st)
+    rows, ld = 1100, (1 << 21) + 8
+    for cols in (40, 61):
+        x = torch.randn((rows, cols), generator=torch.Generator().manual_seed(cols)).to(TYPES[st])
+        src = torch.zeros((rows, ld), dtype=TYPES[st], device=DEV)
+        src[:, :cols] = x.to(DEV)
+        near = quantize(x.to(DEV), cols)
+        far = quantize(src, cols, ld, values=src)
+        assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])
+        assert torch.equal(src[:, :cols], near[2]) and (src[:, cols:cols + 64] == 0).all()
+        del src, far
+
+
+def test_quantize_on_streams_and_in_graphs():
+    say("quantize: streams, graph replays")
+    x = torch.randn((300, 1001), generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    first = quantize(x, 1001, 0, 1024)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.full_like(t, 5) for t in first] for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, o in zip(streams, outs):
+            E.engram_quantize_mx4(x, E.BF16, 300, 1001, 0, 1024, *o, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, first))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        E.engram_quantize_mx4(x, E.BF16, 300, 1001, 0, 1024, *outs[0])
+    for _ in range(3):
+        for t in outs[0]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], first))
+        x.copy_(-x)                     # other values through the same graph
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], quantize(x, 1001, 0, 1024)))
+        x.copy_(-x)
+
+
 # ---- product -----------------------------------------------------------------------
 
 def e4m3_value(c):
@@ -233,7 +277,8 @@ def test_project_without_a_workspace(fmt, tokens, K, N):
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
 @pytest.mark.parametrize("tokens,K,N", [(3, 384, 40), (70, 640, 136), (256, 1152, 520), (700, 512, 1288),
-                                        (5000, 256, 3336), (2100, 640, 4104), (2305, 2176, 4360), (250, 4992, 16392)])
+                                        (5000, 256, 3336), (2100, 640, 4104), (2305, 2176, 4360), (250, 4992, 16392),
+                                        (30_000, 512, 2568)])
 def test_project_integers_are_exact(fmt, tokens, K, N):
     """Codes of halves and integers at scale 1: every partial sum is a multiple of 1/4
     below 2^16, so fp32 holds it and only the bf16 rounding remains."""
@@ -309,7 +354,7 @@ def test_project_zero_tokens_and_rows_behind():
 
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
-@pytest.mark.parametrize("tokens", [1, 40, 256, 600])
+@pytest.mark.parametrize("tokens", [1, 40, 256, 600, 10_000])
 def test_project_same_bits_on_streams_and_in_graphs(fmt, tokens):
     say("project: streams, graph replays", fmt, tokens)
     K, N = 640, 1032
@@ -351,6 +396,30 @@ def test_project_full_layer_sizes():
         e, es, ev = operand(tokens, K, fmt, 14)
         say(fmt, tokens)
         assert_product(project(dev(e), dev(es), fmt, wd, wsd, tokens, K, N)[:, cols], ev, wv[cols], fmt)
+
+
+@pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
+@pytest.mark.parametrize("tokens,K,N", [(90_000, 128, 25600), (1_100_000, 2048, 16)])
+def test_project_offsets_beyond_31_bits(fmt, tokens, K, N):
+    """More than 2^31 outputs, and more than 2^31 bytes of E4M3 inputs (2^30 of E2M1):
+    rows from every part against float64."""
+    say("project: far offsets", fmt, tokens, K, N)
+    width = K if fmt == E.MX_E4M3 else K // 2
+    gen_ = torch.Generator(device=DEV).manual_seed(15)
+    e = torch.randint(0, 256, (tokens, width), dtype=torch.uint8, device=DEV, generator=gen_)
+    if fmt == E.MX_E4M3:
+        e &= 0xD7                       # magnitudes up to 15, no NaN
+    es = torch.full((tokens, K // 32), 126, dtype=torch.uint8, device=DEV)
+    w, ws, wv = operand(N, K, E.MX_E2M1, 16)
+    kv = project(e, es, fmt, dev(w), dev(ws), tokens, K, N)
+    pick = torch.tensor([0, 1, tokens // 3, tokens // 2 + 5, tokens - 257, tokens - 1], device=DEV)
+    raw = e[pick].cpu().numpy().astype(np.int64)
+    if fmt == E.MX_E4M3:
+        ev = e4m3_value(raw)
+    else:
+        codes = np.stack((raw & 15, raw >> 4), -1).reshape(len(pick), -1)
+        ev = np.where(codes & 8, -1.0, 1.0) * GRID[codes & 7]
+    assert_product(kv[pick], ev * 0.5, wv, fmt)
 
 
 # ---- together ----------------------------------------------------------------------
