@@ -50,101 +50,6 @@ __device__ __forceinline__ f32x16 mfma_unit(i32x8 w, i32x8 e, f32x16 acc, uint32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, e, acc, kFp4, EF, I, (int)ws, I, (int)es);
 }
 
-// ---- few tokens and few columns: the weight straight from memory to registers --------
-// A block takes 32 weight rows against up to 32 tokens; its waves split the inputs
-// (unit u belongs to wave u % waves) and their sums meet in LDS in wave order. Each
-// weight byte is loaded once, by the lane that multiplies it. With so few rows that
-// every CU has one block at most, splitting K over the waves beats the next kernel's
-// long pipeline (5120 x 6144 at 1 token: 7.7 against 11.1 us, 12800 x 6144: 12.9
-// against 11.8).
-constexpr int kThinWaves = 4;
-
-template <int EF>
-struct ThinUnit {
-  uint4 w[4];
-  uint4 e[EF == kFp4 ? 4 : 8];
-  uint32_t ws, es;
-};
-
-template <int EF>
-__device__ __forceinline__ void thin_load(ThinUnit<EF> &t, const Mx4Operands &op, int unit, int n, int m,
-                                          int h) {
-  const int KB = op.K / 32;
-  const int b = unit * 8 + 4 * h;
-  const bool in = b < KB;
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  const uint8_t *w = op.w_codes + (int64_t)n * (op.K / 2) + b * 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) t.w[i] = in ? reinterpret_cast<const uint4 *>(w)[i] : none;
-  t.ws = in ? *reinterpret_cast<const uint32_t *>(op.w_scales + (int64_t)n * KB + b) : 0x7F7F7F7Fu;
-  if (EF == kFp4) {
-    const uint8_t *e = op.e_codes + (int64_t)m * (op.K / 2) + b * 16;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t.e[i] = in ? reinterpret_cast<const uint4 *>(e)[i] : none;
-  } else {
-    // halves of blocks 8 unit + i and 8 unit + 4 + i
-    const uint8_t *e = op.e_codes + (int64_t)m * op.K + unit * 256 + 16 * h;
-    const bool second = unit * 8 + 4 < KB;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t.e[2 * i % 8] = *reinterpret_cast<const uint4 *>(e + i * 32);
-      t.e[(2 * i + 1) % 8] = second ? *reinterpret_cast<const uint4 *>(e + 128 + i * 32) : none;
-    }
-  }
-  t.es = in ? *reinterpret_cast<const uint32_t *>(op.e_scales + (int64_t)m * KB + b) : 0x7F7F7F7Fu;
-}
-
-template <int EF, int I>
-__device__ __forceinline__ void thin_mfma(f32x16 &acc, const ThinUnit<EF> &t) {
-  const i32x8 e = EF == kFp4 ? fp4_operand(t.e[I]) : fp8_operand(t.e[2 * I % 8], t.e[(2 * I + 1) % 8]);
-  acc = mfma_unit<EF, I>(fp4_operand(t.w[I]), e, acc, t.ws, t.es);
-}
-
-template <int EF>
-__global__ __launch_bounds__(kThinWaves * 64) void mx4_thin_kernel(Mx4Operands op,
-                                                                   uint16_t *__restrict__ kv) {
-  __shared__ float part[kThinWaves - 1][16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = lane & 31, h = lane >> 5;
-  const int n0 = blockIdx.x * 32;
-  // rows past the end repeat the last one; their outputs are not stored
-  const int n = min(n0 + row, op.N - 1), m = min(row, op.M - 1);
-  f32x16 acc;
-#pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  const int units = (op.K + 255) / 256;
-  for (int u = wave; u < units; u += kThinWaves) {
-    ThinUnit<EF> t;
-    thin_load<EF>(t, op, u, n, m, h);
-    thin_mfma<EF, 0>(acc, t);
-    thin_mfma<EF, 1>(acc, t);
-    thin_mfma<EF, 2>(acc, t);
-    thin_mfma<EF, 3>(acc, t);
-  }
-  if (wave > 0) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) part[wave - 1][r][lane] = acc[r];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int w = 0; w < kThinWaves - 1; ++w)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] += part[w][r][lane];
-  // accumulator r: column n0 + 8 (r / 4) + 4 h + r % 4 of token `row`
-  if (row >= op.M) return;
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int c = n0 + g * 8 + h * 4;
-    if (c < op.N) {
-      uint2 v;
-      v.x = engram::pack_bf16x2(acc[g * 4 + 0], acc[g * 4 + 1]);
-      v.y = engram::pack_bf16x2(acc[g * 4 + 2], acc[g * 4 + 3]);
-      *reinterpret_cast<uint2 *>(kv + (int64_t)row * op.N + c) = v;
-    }
-  }
-}
-
 // ---- many tokens: 256 x 256 tiles through LDS ---------------------------------------
 // gemm_mx_kernel's tiles and two-stage schedule on the narrower operands. A K-step
 // is 128 bytes of an e row: 256 inputs of E2M1 or 128 of E4M3, and 128 or 64 bytes of
@@ -445,48 +350,56 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
   wide_walk<EF>(op, kv, tiles_m, tiles_n);
 }
 
-// ---- up to 256 tokens: columns dealt to every CU, the weight streamed far ahead ------
-// A block takes 128 MT tokens against 32 NI weight rows over the whole of K, so the
-// weight crosses HBM once per token tile. Wave w owns tokens [32 MT w, 32 MT (w + 1))
-// and all the rows. K-steps of 128 inputs; both operands go global -> LDS by direct
-// loads into rings of their own: the weight, which comes from HBM, kRw pairs of steps
-// deep (whole cache lines of a row; by the step, in half lines, 256 tokens took 52 us
-// for 51), e, which every block reads and L2 holds, kRe steps. The one barrier of
-// a step stands before its last MFMAs: by then the step's slots have been read and take
-// the loads of the pair kRw ahead and of step kt + kRe, and step kt + 1 has landed
-// (loads complete in order: all but the kRe - 2 latest batches, and the scales where
-// they were requested among those).
-// Scales go straight to registers, 16 bytes of a row (4 steps) at a time and a group
-// ahead.
-template <int EF>
+// ---- fewer blocks than CUs: small tiles, the operands streamed far ahead -------------
+// A block takes 64 MT tokens against 64 NI weight rows over the whole of K, two waves
+// along each, so that a wave holds 32 MT x 32 NI outputs. K-steps of 128 inputs; both
+// operands go global -> LDS by direct loads into rings of their own: the weight, which
+// comes from HBM, kRw pairs of steps deep (whole cache lines of a row), e, which the
+// blocks of a token tile share and L2 holds, kRe steps. The one barrier of a step stands
+// before its last MFMAs: by then the step's slots have been read and take the loads of
+// step kt + kRe and of the pair kRw ahead, and step kt + 1 has landed. Loads complete in
+// order, so the wait for an e batch is one for every weight load issued before it: e is
+// requested first, which leaves the weight one step more (100 tokens of E4M3: 24 us for
+// 26). Scales go straight to registers, 16 bytes of a row (4 steps) at a time and a
+// group ahead.
+// 256 tokens of E4M3 against 25600 rows of 6144 take 39-42 us, 34 with every load and
+// LDS read left out (launch, ends and MFMAs: the matrix units are busy 45 % of the 200
+// CUs' cycles, and barriers and issue take the rest); E2M1 31, 22 without loads and
+// reads, 28 without the weight's stream alone. 1 token takes 15 us, 5.6 TB/s.
+template <int EF, int NI>
 struct SkinnyCfg {
   static constexpr int kERow = EF == kFp4 ? 64 : 128;   // bytes of an e row and step
-  static constexpr int kRe = EF == kFp4 ? 4 : 3;
-  static constexpr int kRw = EF == kFp4 ? 4 : 3;
-  static constexpr int kUnroll = EF == kFp4 ? 8 : 12;   // steps: a multiple of both rings and of 4
+  static constexpr int kRe = 4;
+  static constexpr int kRw = EF == kFp4 && NI < 4 ? 4 : 3;
+  static constexpr int kUnroll = kRw == 4 ? 8 : 12;     // steps: a multiple of both rings and of 4
 };
 
 template <int EF, int NI, int MT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
-  using Cfg = SkinnyCfg<EF>;
+  using Cfg = SkinnyCfg<EF, NI>;
   constexpr int kRe = Cfg::kRe, kRw = Cfg::kRw, kERow = Cfg::kERow;
-  constexpr int kRows = 32 * NI, kToks = 128 * MT;
+  constexpr int kRows = 64 * NI, kToks = 64 * MT;
   constexpr int kWLoads = kRows * 128 / 1024 / 4;       // direct loads of a wave and pair
   constexpr int kELoads = kToks * kERow / 1024 / 4;     // of a wave and step
   constexpr int kERows = 1024 / kERow;                  // e rows of a direct load
   constexpr int kSLoads = NI + MT;                      // scale loads of four steps
   // one LDS variable per slot: the compiler tells direct loads into up to eight apart
   __shared__ __align__(1024) uint8_t w0[kRows * 128], w1[kRows * 128], w2[kRows * 128];
-  __shared__ __align__(1024) uint8_t w3[EF == kFp4 ? kRows * 128 : 16];
-  __shared__ __align__(1024) uint8_t e0[kToks * kERow], e1[kToks * kERow], e2[kToks * kERow];
-  __shared__ __align__(1024) uint8_t e3[EF == kFp4 ? kToks * kERow : 16];
-  const int n0 = (int)(blockIdx.x % tiles_n) * kRows, m0 = (int)(blockIdx.x / tiles_n) * kToks;
+  __shared__ __align__(1024) uint8_t w3[kRw == 4 ? kRows * 128 : 16];
+  __shared__ __align__(1024) uint8_t e0[kToks * kERow], e1[kToks * kERow];
+  __shared__ __align__(1024) uint8_t e2[kToks * kERow], e3[kToks * kERow];
+  // The token tiles of the same rows go to one XCD, eight row tiles at a time.
+  const int tiles_m = (int)gridDim.x / tiles_n;
+  const int ahead = (int)blockIdx.x / (8 * tiles_m) * 8, left = (int)blockIdx.x - ahead * tiles_m;
+  const int wide = min(8, tiles_n - ahead);
+  const int n0 = (ahead + left % wide) * kRows, m0 = left / wide * kToks;
   const int KB = op.K / 32, KT = op.K / 128;
   const int w_ld = op.K / 2, e_ld = EF == kFp4 ? op.K / 2 : op.K;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave >> 1, wm = wave & 1;
   const int frow = lane & 31, h = lane >> 5;
   const int rows_w = min(kRows, op.N - n0), rows_e = min(kToks, op.M - m0);
   const __amdgpu_buffer_rsrc_t rsW = __builtin_amdgcn_make_buffer_rsrc(
@@ -506,8 +419,8 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   const int e_v1 = EF == kFp4 ? e_v0 : (wave * (kToks / 4) + (lane >> 3)) * e_ld + (c128 ^ 1) * 16;
   const int a_sw = (frow & 7) ^ ((frow >> 3) & 1);
   const int b_sw = EF == kFp4 ? (frow >> 1) & 3 : a_sw;
-  const int a_base = frow * 128, b_base = (wave * 32 * MT + frow) * kERow;
-  const int ws_v = frow * KB, es_v = (wave * 32 * MT + frow) * KB;
+  const int a_base = (wn * 32 * NI + frow) * 128, b_base = (wm * 32 * MT + frow) * kERow;
+  const int ws_v = (wn * 32 * NI + frow) * KB, es_v = (wm * 32 * MT + frow) * KB;
 
 #define MK_W(s) ((s) == 0 ? w0 : (s) == 1 ? w1 : (s) == 2 ? w2 : w3)
 #define MK_E(s) ((s) == 0 ? e0 : (s) == 1 ? e1 : (s) == 2 ? e2 : e3)
@@ -539,6 +452,8 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   _Pragma("unroll") for (int i = 0; i < NI; ++i) _Pragma("unroll") for (int j = 0; j < MT; ++j) \
     acc[i][j] = mfma_unit<EF, s>(fa[i], fb[j], acc[i][j], sa[i], sb[j]);
 #define MK_FENCE() __builtin_amdgcn_sched_barrier(0)
+// what computes may cross, loads may not: the waits count on their order
+#define MK_ORDER() __builtin_amdgcn_sched_barrier(0x000F)
 #define MK_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier(mask, n, 0)
 
   f32x16 acc[NI][MT];
@@ -556,19 +471,31 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   for (int i = 0; i < NI; ++i) ws[i] = wsn[i];
 #pragma unroll
   for (int j = 0; j < MT; ++j) es[j] = esn[j];
-  MK_LOADW(0, 0) MK_LOADE(0, 0) MK_LOADE(1, 1)
-  MK_LOADW(1, 1) MK_LOADE(2, 2)
-  if constexpr (EF == kFp4) { MK_LOADE(3, 3) }
-  MK_LOADW(2, 2)
-  if constexpr (EF == kFp4) { MK_LOADW(3, 3) }
+  // in the order in which the steps before the first would have issued them
+  MK_LOADW(0, 0)
+  if constexpr (kRw == 4) { MK_LOADW(1, 1) }
+  MK_LOADE(0, 0)
+  MK_FENCE();
+  MK_LOADE(1, 1)
+  MK_FENCE();
+  MK_LOADW(kRw - 2, kRw - 2)
+  MK_FENCE();
+  MK_LOADE(2, 2)
+  MK_FENCE();
+  MK_LOADE(3, 3)
+  MK_FENCE();
+  MK_LOADW(kRw - 1, kRw - 1)
+  MK_FENCE();
   // step 0 has landed when only what was issued after it is outstanding
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kRe - 1) * kELoads + (kRw - 1) * kWLoads)
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((kRe - 1) * kELoads + 2 * kWLoads)
                : "memory");
   MK_FENCE();
   MK_FRAGS(0, 0, fa0, fb0)
-// What may be outstanding at step u's barrier: the batches of the kRe - 2 steps before
-// it, the weight's among them (issued at odd steps), and the scales (at every fourth).
-#define MK_PENDING(u)                                                                            ((kRe - 2) * kELoads + (kRe == 4 || (u) % 2 == 0 ? kWLoads : 0) + ((u) % 4 <= kRe - 3 ? kSLoads : 0))
+// What may be outstanding at step u's barrier: everything issued behind the e batch of
+// step u + 1, which is that of step u + 1 - kRe: kRe - 2 batches, the weight's of the
+// odd steps from that one on, the scales (every fourth step) of the steps behind it.
+#define MK_PENDING(u) \
+  ((kRe - 2) * kELoads + ((u) % 2 == 0 ? 2 : 1) * kWLoads + ((u) % 4 <= kRe - 2 ? kSLoads : 0))
 // Step kt + u. The LDS reads come before the direct loads of the same step, whose
 // slots the compiler believes to be in flight (it cannot see the barrier's wait).
 #define MK_STEP(u)                                                                             \
@@ -583,8 +510,11 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
     MK_FENCE();                                                                                \
     MK_FRAGS((u) + 1, 0, fa0, fb0)                                                             \
     MK_FENCE();                                                                                \
-    if ((u) % 2 == 1) { MK_LOADW((kt + (u)) / 2 + kRw, (u) / 2 % kRw) }                        \
     MK_LOADE(kt + (u) + kRe, (u) % kRe)                                                        \
+    if ((u) % 2 == 1) {                                                                        \
+      MK_ORDER();                                                                              \
+      MK_LOADW((kt + (u)) / 2 + kRw, (u) / 2 % kRw)                                            \
+    }                                                                                          \
     MK_MFMA(1, fa1, fb1)                                                                       \
     _Pragma("unroll") for (int g_ = 0; g_ < 8; ++g_) { MK_GROUP(0x008, 1); MK_GROUP(0x020, 2); } \
     MK_FENCE();                                                                                \
@@ -610,6 +540,7 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
 #undef MK_STEP
 #undef MK_PENDING
 #undef MK_GROUP
+#undef MK_ORDER
 #undef MK_FENCE
 #undef MK_MFMA
 #undef MK_FRAGS
@@ -627,7 +558,7 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   static_assert(EF == kFp4 ? kPatch <= kToks * kERow : 2 * kPatch <= kToks * kERow, "patches fit the e slots");
   uint8_t *mine = EF == kFp4 ? (wave == 0 ? e0 : wave == 1 ? e1 : wave == 2 ? e2 : e3)
                              : (wave < 2 ? e0 : e1) + (wave & 1) * kPatch;
-  const int col = n0 + (lane % kChunks) * 8;
+  const int col = n0 + wn * 32 * NI + (lane % kChunks) * 8;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
 #pragma unroll
@@ -645,7 +576,7 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
       const int t = (q * 64 + lane) / kChunks;
       const engram::u32x4 v = *reinterpret_cast<const engram::u32x4 *>(
           mine + (t * kChunks + ((lane % kChunks) ^ (t & (kChunks - 1)))) * 16);
-      const int m = m0 + wave * 32 * MT + j * 32 + t;
+      const int m = m0 + wm * 32 * MT + j * 32 + t;
       if (m < op.M && col < op.N)
         __builtin_nontemporal_store(v, reinterpret_cast<engram::u32x4 *>(kv + (int64_t)m * op.N + col));
     }
@@ -654,36 +585,30 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
 
 template <int EF, int NI, int MT>
 hipError_t launch_skinny(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
-  const int tiles_n = (op.N + 32 * NI - 1) / (32 * NI), tiles_m = (op.M + 128 * MT - 1) / (128 * MT);
+  const int tiles_n = (op.N + 64 * NI - 1) / (64 * NI), tiles_m = (op.M + 64 * MT - 1) / (64 * MT);
   hipLaunchKernelGGL((mx4_skinny_kernel<EF, NI, MT>), dim3((unsigned)(tiles_n * tiles_m)), dim3(256), 0,
                      stream, op, kv, tiles_n);
   return hipGetLastError();
 }
 
-// Which kernel: up to 32 tokens and one block of 32 rows per CU, the thin one. Up to 256
-// tokens, or where its blocks fit the CUs at once, the skinny one (600 tokens x 5120
-// columns of E4M3: 27 us against 61 in whole tiles; 512 x 25600, two blocks a CU: 84
-// against 73), with 64 weight rows a block where those fit the CUs, else 128, which
-// halves e's traffic. Above, whole 256 x 256 tiles.
+// The smallest tile whose blocks fit the CUs at once: a larger one leaves CUs idle and, at
+// few tokens, multiplies padding (us, E4M3, 6144 inputs: 1 token x 25600 columns 20, 15,
+// 20, 34 with tiles of 64 x 64, 64 x 128, 128 x 128, 128 x 256 tokens x rows; 100 x 5120
+// 11, 11, 18, 31; 600 x 5120 41, 29, 22, 36). Where no such tile fits, the largest up to
+// 256 tokens, above whole 256 x 256 tiles (300 x 20480, 240 blocks of 128 x 256: 42 us
+// against 64 in whole tiles; 300 x 25600, 300 blocks: 75 against 66).
 template <int EF>
 hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
   int cus = 0;
   const hipError_t err = cu_count(cus);
   if (err != hipSuccess) return err;
-  if (op.M <= 32 && op.N <= 32 * cus) {
-    hipLaunchKernelGGL((mx4_thin_kernel<EF>), dim3((unsigned)((op.N + 31) / 32)), dim3(kThinWaves * 64), 0,
-                       stream, op, kv);
-    return hipGetLastError();
-  }
-  const auto blocks = [&](int rows) {
-    return (int64_t)((op.M + 255) / 256) * ((op.N + rows - 1) / rows);
+  const auto fits = [&](int toks, int rows) {
+    return ((int64_t)op.M + toks - 1) / toks * (((int64_t)op.N + rows - 1) / rows) <= cus;
   };
-  if (op.M <= 256 || blocks(128) <= cus) {
-    const bool narrow = blocks(64) <= cus;
-    if (op.M <= 128)
-      return narrow ? launch_skinny<EF, 2, 1>(op, kv, stream) : launch_skinny<EF, 4, 1>(op, kv, stream);
-    return narrow ? launch_skinny<EF, 2, 2>(op, kv, stream) : launch_skinny<EF, 4, 2>(op, kv, stream);
-  }
+  if (fits(64, 64)) return launch_skinny<EF, 1, 1>(op, kv, stream);
+  if (fits(64, 128)) return launch_skinny<EF, 2, 1>(op, kv, stream);
+  if (fits(128, 128)) return launch_skinny<EF, 2, 2>(op, kv, stream);
+  if (op.M <= 256 || fits(128, 256)) return launch_skinny<EF, 4, 2>(op, kv, stream);
   const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   const bool even = (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep % 2 == 0;

@@ -258,7 +258,7 @@ SHAPES = [(1, 128, 8), (1, 6144, 520), (2, 256, 40), (7, 384, 24), (31, 640, 264
           (129, 640, 392), (255, 1024, 520), (256, 6144, 1032), (257, 256, 264), (300, 384, 776),
           (513, 1280, 2056), (1003, 896, 520), (1, 20480, 32), (2500, 128, 264), (40, 256, 12808),
           (20, 1664, 16392), (100, 1920, 16400), (200, 1408, 16648), (2100, 128, 4104), (2049, 384, 4360),
-          (2305, 1152, 4104), (2111, 1280, 4128)]
+          (2305, 1152, 4104), (2111, 1280, 4128), (130, 256, 33032), (300, 640, 20488)]
 
 
 @pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
