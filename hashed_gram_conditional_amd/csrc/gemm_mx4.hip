@@ -494,19 +494,26 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
 // What may be outstanding at step u's barrier: everything issued behind the e batch of
 // step u + 1, which is that of step u + 1 - kRe: kRe - 2 batches, the weight's of the
 // odd steps from that one on, the scales (every fourth step) of the steps behind it.
-#define MK_PENDING(u) \
-  ((kRe - 2) * kELoads + ((u) % 2 == 0 ? 2 : 1) * kWLoads + ((u) % 4 <= kRe - 2 ? kSLoads : 0))
-// Step kt + u. The LDS reads come before the direct loads of the same step, whose
+// Only loads that the compiler must issue, and issue there, may be counted: the direct
+// loads write LDS and stay where they are, and a scale load of the main loop is read by
+// a later turn. A scale load of the last steps is not counted: the compiler may move one to
+// where it is read, and deletes one that no step reads.
+#define MK_PENDING(u, last)                                        \
+  ((kRe - 2) * kELoads + ((u) % 2 == 0 ? 2 : 1) * kWLoads +        \
+   (!(last) && (u) % 4 <= kRe - 2 ? kSLoads : 0))
+// Step kt + u, of the main loop or of the last steps, which end before the next group of
+// scales is due. The LDS reads come before the direct loads of the same step, whose
 // slots the compiler believes to be in flight (it cannot see the barrier's wait).
-#define MK_STEP(u)                                                                             \
+#define MK_STEP(u, last)                                                                       \
   {                                                                                            \
-    if ((u) % 4 == 0) { MK_SCALES((kt + (u)) / 4 + 1) }                                        \
+    if ((u) % 4 == 0 && (!(last) || (u) + 4 < Cfg::kUnroll)) { MK_SCALES((kt + (u)) / 4 + 1) } \
     _Pragma("unroll") for (int i = 0; i < NI; ++i) sa[i] = MK_WORD(ws[i], (u) % 4) >> (16 * h); \
     _Pragma("unroll") for (int j = 0; j < MT; ++j) sb[j] = MK_WORD(es[j], (u) % 4) >> (16 * h); \
     MK_FRAGS(u, 1, fa1, fb1)                                                                   \
     MK_MFMA(0, fa0, fb0)                                                                       \
     MK_FENCE();                                                                                \
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(MK_PENDING(u)) : "memory"); \
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(MK_PENDING(u, last))        \
+                 : "memory");                                                                  \
     MK_FENCE();                                                                                \
     MK_FRAGS((u) + 1, 0, fa0, fb0)                                                             \
     MK_FENCE();                                                                                \
@@ -525,15 +532,21 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
   }
 // The steps behind the last whole unrolling stand apart: branches around steps of the
 // main loop made the compiler wait for every load at each of them.
-#define MK_LAST(u) \
-  if (kt + (u) < KT) MK_STEP(u)
+#define MK_LAST(u)           \
+  if (kt + (u) >= KT) break; \
+  MK_STEP(u, true)
   int kt = 0;
   for (; kt + Cfg::kUnroll <= KT; kt += Cfg::kUnroll) {
-    MK_STEP(0) MK_STEP(1) MK_STEP(2) MK_STEP(3) MK_STEP(4) MK_STEP(5) MK_STEP(6) MK_STEP(7)
-    if constexpr (Cfg::kUnroll == 12) { MK_STEP(8) MK_STEP(9) MK_STEP(10) MK_STEP(11) }
+    MK_STEP(0, false) MK_STEP(1, false) MK_STEP(2, false) MK_STEP(3, false)
+    MK_STEP(4, false) MK_STEP(5, false) MK_STEP(6, false) MK_STEP(7, false)
+    if constexpr (Cfg::kUnroll == 12) {
+      MK_STEP(8, false) MK_STEP(9, false) MK_STEP(10, false) MK_STEP(11, false)
+    }
   }
-  MK_LAST(0) MK_LAST(1) MK_LAST(2) MK_LAST(3) MK_LAST(4) MK_LAST(5) MK_LAST(6)
-  if constexpr (Cfg::kUnroll == 12) { MK_LAST(7) MK_LAST(8) MK_LAST(9) MK_LAST(10) }
+  do {
+    MK_LAST(0) MK_LAST(1) MK_LAST(2) MK_LAST(3) MK_LAST(4) MK_LAST(5) MK_LAST(6)
+    if constexpr (Cfg::kUnroll == 12) { MK_LAST(7) MK_LAST(8) MK_LAST(9) MK_LAST(10) }
+  } while (false);
   // every direct load has landed before the slots hold the outputs
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #undef MK_LAST
