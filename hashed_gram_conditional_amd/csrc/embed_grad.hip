@@ -48,6 +48,7 @@ constexpr int kSumThreads = 256;
 constexpr int kJoinThreads = 512;
 constexpr int kJoinChunks = 8;         // chunks one join block looks after
 constexpr int kFewPieces = 16;         // pieces of a run that one group of threads joins
+constexpr int kJoinFan = 16;           // groups whose sums one group adds at a time
 
 __device__ __forceinline__ uint32_t key_of(int64_t id, int64_t table_rows) {
   return (uint64_t)id < (uint64_t)table_rows ? (uint32_t)id : (uint32_t)table_rows;
@@ -672,8 +673,12 @@ __device__ __forceinline__ void add_pieces(const float *__restrict__ pieces, int
 // The long runs: block b joins the pieces of those that begin in its kJoinChunks
 // chunks. The threads form groups of one thread per column (4 columns where VEC is
 // 4). A run of few pieces is one group's, added in order; of a longer one each group
-// adds a fixed share of the pieces in order, and the first group adds the groups
-// in order. Also closes the list of rows with -1.
+// adds a fixed share of the pieces in order, every kJoinFan-th one the groups up to the
+// next such, and the first group those. With 8 to 512 groups a term of a run of m so
+// passes through fewer than 200 + m / 64 additions: 64 of its chunk, m / (8 * 8) + 2 of its
+// group, 16 and 32 of the groups. (The first group adding all of them, 512 for narrow
+// rows, took 4096 ids of one row through 520, and 29 us for 25 at one column.)
+// Also closes the list of rows with -1.
 template <int VEC>
 __global__ __launch_bounds__(kJoinThreads) void join_pieces_kernel(
     Runs r, Sums s, const float *__restrict__ pieces, int64_t piece_ld, int cols, int width,
@@ -735,8 +740,17 @@ __global__ __launch_bounds__(kJoinThreads) void join_pieces_kernel(
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sums[e * kJoinThreads + tid] = acc[e];
     __syncthreads();
+    if (active && group % kJoinFan == 0) {
+      for (int q = group + 1; q < min(group + kJoinFan, groups); ++q) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += sums[e * kJoinThreads + q * width + tid - group * width];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sums[e * kJoinThreads + tid] = acc[e];
+    }
+    __syncthreads();
     if (active && group == 0) {
-      for (int q = 1; q < groups; ++q) {
+      for (int q = kJoinFan; q < groups; q += kJoinFan) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] += sums[e * kJoinThreads + q * width + tid];
       }

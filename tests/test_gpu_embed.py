@@ -440,3 +440,22 @@ def test_dense_gradient_in_a_graph(n, R, table_ld):
         step()
         torch.cuda.synchronize()
         assert torch.equal(grad, first)
+
+
+# ---- the order of a long sum --------------------------------------------------------
+
+@pytest.mark.parametrize("ot", [E.BF16, E.F32])
+@pytest.mark.parametrize("dim,m", [(1, 4096), (2, 2048), (3, 1400), (8, 2048), (16, 1024), (256, 4096),
+                                   (1, 32768), (8, 40_000)])
+def test_grad_additions_of_one_row(ot, dim, m):
+    """One row named by every id: 1 and then, in every chunk of 8, one value just below
+    half a step of 1. A value added to the 1 by itself is lost, so the error counts the
+    additions that stand one behind another, of which there are fewer than 200 + m / 64."""
+    say("grad: additions", ot, dim, m)
+    d_out = torch.zeros((m, dim), dtype=TYPES[ot])
+    d_out[::8] = 0.984375 * 2.0 ** -24               # 63 / 64, exact in bf16
+    d_out[0] = 1.0
+    rows, grad, count = _grad(torch.zeros(m, dtype=torch.int64), d_out, 1, dim, ot, 1.0)
+    assert count == 1 and rows[0] == 0
+    want = d_out.double().sum(0)
+    assert ((grad[0].double() - want).abs() <= (200 + m / 64) * U32 * want).all()
