@@ -459,3 +459,60 @@ def test_grad_additions_of_one_row(ot, dim, m):
     assert count == 1 and rows[0] == 0
     want = d_out.double().sum(0)
     assert ((grad[0].double() - want).abs() <= (200 + m / 64) * U32 * want).all()
+
+
+# ---- longer chunks -------------------------------------------------------------------
+
+def plan_chunk(n, per_chunk):
+    """Positions of a chunk: 64, halved down to 8 until the chunks' threads (one per 8
+    columns) number 2048 per CU."""
+    chunk = 64
+    while chunk > 8 and n // chunk * per_chunk < 256 * 2048:
+        chunk //= 2
+    return chunk
+
+
+@pytest.mark.parametrize("ot", [E.BF16, E.F32])
+@pytest.mark.parametrize("n,dim,chunk", [(40_000, 2048, 16), (30_000, 2824, 16), (70_000, 2048, 32),
+                                         (786_432, 256, 32), (140_000, 2048, 64), (1_050_000, 256, 64)])
+def test_grad_run_lengths_of_longer_chunks(ot, n, dim, chunk):
+    """Runs of both sides of the longest that one thread sums (twice a chunk, at most 64), of
+    16 pieces and of thousands, among rows named once or a few times: row ids, count and
+    gradients, sparse and dense, a sample of columns against float64."""
+    say("grad: chunk", chunk, ot, n, dim)
+    assert plan_chunk(n, dim // 8) == chunk
+    longest = min(2 * chunk, 64)
+    marks = [longest - 1, longest, longest + 1, chunk - 1, chunk, chunk + 1, 15 * chunk, 16 * chunk,
+             16 * chunk + 1, 17 * chunk, 18 * chunk + 3, 40 * chunk, 1, 2, 100 * chunk - 1]
+    hot = n // 8
+    rng = np.random.default_rng(n + dim)
+    lengths = np.concatenate([np.repeat(marks, 3), [hot, hot // 3]])
+    rest = rng.zipf(1.3, n - int(lengths.sum()) - 97)
+    R = 3 * lengths.size + 5000
+    ids = np.concatenate([np.repeat(rng.permutation(lengths.size) * 3, lengths),
+                          3 * lengths.size + np.minimum(rest - 1, 4999),
+                          np.full(97, -1)])
+    ids = torch.from_numpy(rng.permutation(ids).astype(np.int64))
+    g = torch.Generator(device=DEV).manual_seed(n)
+    d_out = torch.empty((n, dim), dtype=TYPES[ot], device=DEV).normal_(generator=g)
+    cols = torch.tensor([0, 1, 7, 8, 63, dim // 2 + 3, dim - 9, dim - 8, dim - 1], device=DEV)
+    er, es, tol = _reference(ids, d_out[:, cols].cpu(), R, 0.75)
+    d = E.embed_desc(R, n, dim, E.F32, ot, 0.75)
+    size = E.engram_embed_grad_workspace_size(d)
+    ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV)
+    rows = torch.full((n,), 99, dtype=torch.int64, device=DEV)
+    grad = torch.full((n, dim), 7.0, device=DEV)
+    count = torch.full((1,), 99, dtype=torch.int64, device=DEV)
+    dids = ids.to(DEV)
+    E.engram_embed_grad(d, d_out, dids, rows, grad, count, ws, size)
+    full = torch.full((R, dim), 3.0, device=DEV)
+    E.engram_embed_grad_dense(d, d_out, dids, full, 0, ws, size)
+    torch.cuda.synchronize()
+    assert int(count) == er.size
+    assert np.array_equal(rows[:er.size].cpu().numpy(), er) and (rows[er.size:] == -1).all()
+    assert ((grad[:er.size][:, cols].double().cpu() - es).abs() <= tol).all()
+    assert (grad[er.size:] == 7.0).all()
+    touched = torch.from_numpy(er).to(DEV)
+    assert torch.equal(full[touched], grad[:er.size])
+    full[touched] = 0
+    assert (full == 0).all()
