@@ -216,11 +216,14 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object (2.9 us a call, against
-        # 0.2 us for its handle alone and 4 us for a whole small entry point)
+        # 0.2 us for its handle alone and 4 us for a whole small entry point). The
+        # handle's function is not part of torch's public interface: without it, the
+        # public way.
         import torch
-        if not torch.cuda.is_initialized():
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if handle is None or not torch.cuda.is_initialized():
             return torch.cuda.current_stream().cuda_stream
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return handle(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
