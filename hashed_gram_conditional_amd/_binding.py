@@ -213,17 +213,27 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, on=None) -> Optional[int]:
+    """Handle of a stream, the current one for None. A buffer ``on`` another device than
+    the current one is refused there: the kernels would run on a device that need not
+    reach it, in no order with its own work."""
     if stream is None:
         # torch.cuda.current_stream() builds a Stream object (2.9 us a call, against
         # 0.2 us for its handle alone and 4 us for a whole small entry point). The
-        # handle's function is not part of torch's public interface: without it, the
-        # public way.
+        # handle's and the device's functions are not part of torch's public interface:
+        # without them, the public way.
         import torch
+        device = getattr(torch._C, "_cuda_getDevice", None)
         handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if handle is None or not torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
-        return handle(torch.cuda.current_device())
+        if device is None or handle is None or not torch.cuda.is_initialized():
+            here, stream = torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+        else:
+            here = device()
+            stream = handle(here)
+        if on is not None and not isinstance(on, int) and on.is_cuda and on.get_device() != here:
+            raise ValueError(f"engram: buffers on cuda:{on.get_device()}, but the current device is "
+                             f"cuda:{here}: make theirs current or pass a stream of it")
+        return stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -493,7 +503,7 @@ def engram_forward_conv(params: HashParams, desc: ForwardDesc, conv: ShortConv, 
 def engram_embed(desc: EmbedDesc, table, row_ids, out, stream=None):
     """out[i] = scale * table[row_ids[i]]; zero rows for ids outside the table."""
     _check(LIB.engram_embed(ctypes.byref(desc), _table_ptr(table), _ptr(row_ids), _ptr(out),
-                            _stream(stream)), "engram_embed")
+                            _stream(stream, out)), "engram_embed")
 
 
 def engram_embed_grad_workspace_size(desc: EmbedDesc) -> int:
@@ -505,7 +515,7 @@ def engram_embed_grad(desc: EmbedDesc, d_out, row_ids, grad_rows, grad, n_rows, 
     """The touched rows in ascending order (then -1), their fp32 gradients and their number."""
     _check(LIB.engram_embed_grad(ctypes.byref(desc), _ptr(d_out), _ptr(row_ids), _ptr(grad_rows),
                                  _ptr(grad), _ptr(n_rows), _ptr(workspace), workspace_bytes,
-                                 _stream(stream)), "engram_embed_grad")
+                                 _stream(stream, grad)), "engram_embed_grad")
 
 
 def engram_embed_grad_dense(desc: EmbedDesc, d_out, row_ids, grad, accumulate: int, workspace,
@@ -513,14 +523,14 @@ def engram_embed_grad_dense(desc: EmbedDesc, d_out, row_ids, grad, accumulate: i
     """The fp32 gradient of the whole table, overwritten (0) or added to (1)."""
     _check(LIB.engram_embed_grad_dense(ctypes.byref(desc), _ptr(d_out), _ptr(row_ids), _ptr(grad),
                                        accumulate, _ptr(workspace), workspace_bytes,
-                                       _stream(stream)), "engram_embed_grad_dense")
+                                       _stream(stream, grad)), "engram_embed_grad_dense")
 
 
 def engram_quantize_mx4(src, src_type: int, rows: int, cols: int, src_ld: int, out_cols: int,
                         codes, scales, values=None, stream=None):
     """E2M1 codes and E8M0 block scales of src (and the values they stand for)."""
     _check(LIB.engram_quantize_mx4(_ptr(src), src_type, rows, cols, src_ld, out_cols, _ptr(codes),
-                                   _ptr(scales), _ptr(values), _stream(stream)),
+                                   _ptr(scales), _ptr(values), _stream(stream, codes)),
            "engram_quantize_mx4")
 
 
@@ -535,5 +545,5 @@ def engram_project_mx4(e_codes, e_scales, e_format: int, w_codes, w_scales, kv, 
     """The projection with a 4-bit weight (e in 8 or 4 bits)."""
     _check(LIB.engram_project_mx4(_ptr(e_codes), _ptr(e_scales), e_format, _ptr(w_codes),
                                   _ptr(w_scales), _ptr(kv), tokens, in_dim, out_dim,
-                                  _ptr(workspace), workspace_bytes, _stream(stream)),
+                                  _ptr(workspace), workspace_bytes, _stream(stream, kv)),
            "engram_project_mx4")

@@ -45,6 +45,7 @@
  *     out-of-range rows output zero rows). The gate decides DEAD positions from
  *     the raw id alone, so a map must pass engram_check_token_map first.
  *   - Calls that write overlapping buffers on different streams race.
+ *   - The current device is the one that holds the buffers and the stream.
  *
  * Host-resident tables ([P1] "放在第 1 层和第 14 层", last paragraph: the rows a
  * step needs depend on the token ids alone, so the table can stay in host memory
