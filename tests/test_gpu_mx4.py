@@ -469,3 +469,43 @@ def test_table_rows_codes_project_directly():
     rows = raw[ids].astype(np.int64)
     vals = e4m3_value(rows[:, :256]) * np.repeat(2.0 ** (rows[:, 256:] - 127.0), 32, axis=1)
     assert_product(kv, vals.reshape(tokens, -1), wv, E.MX_E4M3)
+
+
+@pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
+@pytest.mark.parametrize("tokens,K,N", [(1, 6144, 264), (129, 896, 392), (256, 1408, 16648), (2111, 1280, 4128)])
+def test_project_leaves_a_given_workspace_alone(fmt, tokens, K, N):
+    say("project: a real workspace", fmt, tokens, K, N)
+    e, es, _ = operand(tokens, K, fmt, 31)
+    w, ws, _ = operand(N, K, E.MX_E2M1, 32)
+    args = [dev(x) for x in (e, es, w, ws)]
+    plain = project(args[0], args[1], fmt, args[2], args[3], tokens, K, N, workspace=False)
+    buf = torch.full((1 << 16,), 0xA5, dtype=torch.uint8, device=DEV)
+    assert buf.data_ptr() % 256 == 0
+    for size in (0, buf.numel()):
+        kv = torch.full_like(plain, 7.0)
+        E.engram_project_mx4(args[0], args[1], fmt, args[2], args[3], kv, tokens, K, N, buf, size)
+        torch.cuda.synchronize()
+        assert torch.equal(kv, plain) and (buf == 0xA5).all()
+
+
+@pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
+@pytest.mark.parametrize("tokens,K,N", [(256, 6144, 25600), (1003, 6144, 25600), (256, 5888, 16400),
+                                        (64, 2816, 12808), (40, 768, 264)])
+def test_project_repeats_itself(fmt, tokens, K, N):
+    """Twelve calls over outputs filled with something else each time, other work between."""
+    say("project: repeats", fmt, tokens, K, N)
+    g = torch.Generator(device=DEV).manual_seed(K)
+    width = K if fmt == E.MX_E4M3 else K // 2
+    e = torch.randint(0, 256, (tokens, width), dtype=torch.uint8, device=DEV, generator=g)
+    if fmt == E.MX_E4M3:
+        e &= 0xF7                       # no NaN
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV, generator=g)
+    es = torch.randint(120, 132, (tokens, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+    ws = torch.randint(120, 132, (N, K // 32), dtype=torch.uint8, device=DEV, generator=g)
+    first = project(e, es, fmt, w, ws, tokens, K, N)
+    assert torch.isfinite(first).all()
+    kv = torch.empty_like(first)
+    for k in range(12):
+        kv.fill_(float(k))
+        E.engram_project_mx4(e, es, fmt, w, ws, kv, tokens, K, N)
+        assert torch.equal(kv, first)
