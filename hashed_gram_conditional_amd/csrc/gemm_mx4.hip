@@ -607,21 +607,27 @@ hipError_t launch_skinny(const Mx4Operands &op, uint16_t *kv, hipStream_t stream
 // The smallest tile whose blocks fit the CUs at once: a larger one leaves CUs idle and, at
 // few tokens, multiplies padding (us, E4M3, 6144 inputs: 1 token x 25600 columns 20, 15,
 // 20, 34 with tiles of 64 x 64, 64 x 128, 128 x 128, 128 x 256 tokens x rows; 100 x 5120
-// 11, 11, 18, 31; 600 x 5120 41, 29, 22, 36). Where no such tile fits, the largest up to
-// 256 tokens, above whole 256 x 256 tiles (300 x 20480, 240 blocks of 128 x 256: 42 us
-// against 64 in whole tiles; 300 x 25600, 300 blocks: 75 against 66).
+// 11, 11, 18, 31; 600 x 5120 41, 29, 22, 36). Where no such tile fits, the blocks come in
+// rounds, a round of whole 256 x 256 tiles as long as 1.6 to 1.9 of 128 x 256: those are taken
+// where their rounds number up to 5 / 3 of the whole tiles' (us, E4M3 and E2M1, 128 x 256
+// against 256 x 256; 1 round: 240 blocks of 300 x 20480, E4M3 42, 64; 2 to 2: 600 x 25600
+// 83, 126 and 63, 85; 3 to 2: 768 x 25600 115, 135 and 86, 91; 2 to 1: 256 x 33024 76, 67
+// and 57, 49; 4 to 2: 1003 x 25600 154, 135 and 114, 94; 7 to 4: 2048 x 25600 281, 285 and
+// 207, 191; with 1024 inputs the same sides win). Up to 128 tokens both sides have as
+// many blocks: 128 x 66048 83, 125 and 68, 84.
 template <int EF>
 hipError_t launch_mx4(const Mx4Operands &op, uint16_t *kv, hipStream_t stream) {
   int cus = 0;
   const hipError_t err = cu_count(cus);
   if (err != hipSuccess) return err;
-  const auto fits = [&](int toks, int rows) {
-    return ((int64_t)op.M + toks - 1) / toks * (((int64_t)op.N + rows - 1) / rows) <= cus;
+  const auto rounds = [&](int toks, int rows) {
+    const int64_t blocks = ((int64_t)op.M + toks - 1) / toks * (((int64_t)op.N + rows - 1) / rows);
+    return (blocks + cus - 1) / cus;
   };
-  if (fits(64, 64)) return launch_skinny<EF, 1, 1>(op, kv, stream);
-  if (fits(64, 128)) return launch_skinny<EF, 2, 1>(op, kv, stream);
-  if (fits(128, 128)) return launch_skinny<EF, 2, 2>(op, kv, stream);
-  if (op.M <= 256 || fits(128, 256)) return launch_skinny<EF, 4, 2>(op, kv, stream);
+  if (rounds(64, 64) == 1) return launch_skinny<EF, 1, 1>(op, kv, stream);
+  if (rounds(64, 128) == 1) return launch_skinny<EF, 2, 1>(op, kv, stream);
+  if (rounds(128, 128) == 1) return launch_skinny<EF, 2, 2>(op, kv, stream);
+  if (3 * rounds(128, 256) <= 5 * rounds(BM, BN)) return launch_skinny<EF, 4, 2>(op, kv, stream);
   const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   const bool even = (op.K + WideCfg<EF>::kStep - 1) / WideCfg<EF>::kStep % 2 == 0;

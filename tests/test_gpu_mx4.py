@@ -509,3 +509,20 @@ def test_project_repeats_itself(fmt, tokens, K, N):
         kv.fill_(float(k))
         E.engram_project_mx4(e, es, fmt, w, ws, kv, tokens, K, N)
         assert torch.equal(kv, first)
+
+
+@pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
+@pytest.mark.parametrize("tokens,K,N", [(128, 384, 66056), (129, 384, 33032), (256, 768, 65800), (600, 896, 25608),
+                                        (768, 1408, 25608), (900, 512, 25608), (1700, 640, 10248),
+                                        (5000, 512, 10248)])
+def test_project_rounds_of_tiles(fmt, tokens, K, N):
+    """Shapes on both sides of the choice between tiles of 128 and 256 tokens, of one round of
+    blocks to four, and tiles walked by a block: exact integer sums as above."""
+    say("project: rounds", fmt, tokens, K, N)
+    e, es, ev = operand(tokens, K, fmt, 41, integer=True)
+    w, ws, wv = operand(N, K, E.MX_E2M1, 42, integer=True)
+    got = project(dev(e), dev(es), fmt, dev(w), dev(ws), tokens, K, N)
+    wt = dev(wv).float().t().contiguous()
+    for m in range(0, tokens, 1024):        # sums of multiples of 1/4 below 2^16: fp32 holds them
+        exact = dev(ev[m:m + 1024]).float() @ wt
+        assert torch.equal(got[m:m + 1024], exact.to(torch.bfloat16))
