@@ -8,7 +8,9 @@
 // latency of random rows. The product is formed in fp32 and rounded once to the
 // output type (nearest, ties to even). Bound by HBM: 786432 rows of 256 from fp32 to
 // bf16 take 189 us (1.02 GB, 5.4 TB/s) with nontemporal stores, which leave the cache
-// to repeated rows, and 211 us with plain ones; four groups a thread 194 us.
+// to repeated rows, and 211 us with plain ones; four groups a thread 194 us. Widths and
+// strides that are not multiples of 8 move value by value: 255 columns take 471 us (2.2
+// TB/s), from bf16 to bf16 453 against 114.
 #include "common.h"
 #include "fast_div.h"
 

@@ -14,17 +14,17 @@
 //   2. Runs of equal keys: run u starts at sorted position starts[u]; the number
 //      of runs is known only on the device.
 //   3. Sums: the sorted positions are cut into chunks of `chunk`; a thread owns
-//      one chunk and 8 (bf16) or 4 (fp32) columns, so neighbouring threads read
-//      whole rows, and walks the runs that begin in its chunk, adding in fp32 in
+//      one chunk and 8 columns (one, where the width or a stride is no whole number
+//      of groups), so neighbouring threads read whole rows, and walks the runs that begin in its chunk, adding in fp32 in
 //      the order of i. A run longer than `longest` is summed piece by piece, a
 //      piece per chunk it touches, and
 //   4. the pieces are joined: fixed groups of pieces in order, then the groups
 //      in order.
 //
 // Bound by HBM in step 3: d_out is read once, a row's sum written once. 786432 ids of
-// 256 bf16 take 300 us: 80 for the sort and the runs, 222 for the sums (1.02 GB, 4.6
-// TB/s), 10 for the join. Small calls are bound by the latency of their five launches:
-// 12216 ids take 28 us.
+// 256 bf16 take 302 us: 69 for the sort and the runs, 223 for the sums (1.02 GB, 4.6
+// TB/s), 10 for the join; 255 columns, one value at a time, 405. Small calls are bound by
+// the latency of their five launches: 12216 ids take 28 us.
 #include "common.h"
 #include "fast_div.h"
 
@@ -869,9 +869,10 @@ hipError_t engram_launch_embed_grad(const EngramEmbedArgs &a, const void *d_out,
     const int merges = parts > 1 ? (int)((p.n + kMergeElems - 1) / kMergeElems) : 0;
     const int tiles = p.n > 0 ? (int)((p.n + kSmallTile - 1) / kSmallTile) : 1;
     uint2 *sorted = pairs[parts > 1 ? 0 : 1];
-    // Clearing is shared out over the three launches, the least to the first, which is
-    // the shortest (99092 x 1024: 100 us in all, 106 with thirds, 108 with most of it in
-    // the first).
+    // Clearing is shared out over the three launches. The shares matter little: with
+    // these, with thirds and with half of it in the first, 8191 ids and 99092 x 1024
+    // values took 98, 101 and 97 us, 509 ids of the same 87, 88 and 84, and 32000 ids of
+    // 99092 x 256 77, 76 and 76.
     z.end = zero_total / 8;
     if (parts + zero_blocks(kPart) > 0)
       hipLaunchKernelGGL(sort_part_kernel, dim3((unsigned)parts + zero_blocks(kPart)), dim3(kPart), 0,

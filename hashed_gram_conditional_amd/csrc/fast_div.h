@@ -1,5 +1,5 @@
 // Division of a 64-bit index by a fixed divisor with one high multiply: with
-// M = floor(2^64 / d) + 1 = (2^64 + e) / d and 1 <= e <= d, hi64(g M) is
+// M = floor((2^64 - 1) / d) + 1 = (2^64 + e) / d and 0 <= e < d, hi64(g M) is
 // floor(g / d) for every g with g d < 2^64, which the callers' size limits keep.
 // d = 1 has no such M and returns g.
 #pragma once

@@ -4,6 +4,14 @@
 // formats as they are, multiplies the codes exactly, applies both block scales and
 // accumulates in fp32; kv is rounded once to bf16.
 //
+// With two E2M1 operands nothing is lost before fp32. With an E4M3 operand the instruction
+// first adds the products of eight consecutive inputs in fixed point, the last place 2^-13
+// of the largest product's power of two. That is taken as it is: 256 tokens x 25600 from
+// 6144 normal inputs lie as far from the 64-bit product as fp32 sums rounded to bf16 do
+// (1.6552e-3 of its norm, both), with 0.4 % of the values on the neighbour of the nearest
+// bf16 (0.001 %). Sums without it need the bf16 instruction, at half the 8-bit rate and on
+// four times W's bytes of LDS.
+//
 // Lane layout of that MFMA (measured on gfx950): lane l of half h = l / 32 holds
 // row l % 32. Its 16 bytes of E2M1 are inputs [32 h, 32 h + 32) of the 64 in order;
 // its 32 bytes of E4M3 are inputs [16 h, 16 h + 16) and [32 + 16 h, 48 + 16 h). The
@@ -63,7 +71,10 @@ __device__ __forceinline__ f32x16 mfma_unit(i32x8 w, i32x8 e, f32x16 acc, uint32
 // stored, and the stores while the next one begins (32768 x 1024 x 25600: 655 -> 560 us,
 // with 6144 inputs 2.57 -> 2.55 ms: there power sets the clock, 1.76 GHz with the matrix
 // units 54 % busy; an MFMA loop of nothing else reaches 6.4 PFLOP/s, with the LDS reads
-// 6.0, this kernel 4.0).
+// 6.0, this kernel 4.0). An odd number of K-steps costs that overlap (32768 x 25600 in us:
+// E4M3 with 8, 9 and 10 steps 764, 911 and 895; E2M1 with 4, 5 and 6 steps 589, 757 and
+// 754). The E4M3 instance keeps 17 registers in scratch memory and reads one of them, an
+// LDS address, in every K-step, with a wait in front of 11 of its 12 direct loads.
 template <int EF>
 struct WideCfg {
   static constexpr int kStep = EF == kFp4 ? 256 : 128;      // inputs of a K-step
@@ -350,7 +361,7 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
   wide_walk<EF>(op, kv, tiles_m, tiles_n);
 }
 
-// ---- fewer blocks than CUs: small tiles, the operands streamed far ahead -------------
+// ---- few blocks: small tiles, the operands streamed far ahead ------------------------
 // A block takes 64 MT tokens against 64 NI weight rows over the whole of K, two waves
 // along each, so that a wave holds 32 MT x 32 NI outputs. K-steps of 128 inputs; both
 // operands go global -> LDS by direct loads into rings of their own: the weight, which
@@ -362,9 +373,9 @@ void mx4_wide_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_m, int
 // requested first, which leaves the weight one step more (100 tokens of E4M3: 24 us for
 // 26). Scales go straight to registers, 16 bytes of a row (4 steps) at a time and a
 // group ahead.
-// 256 tokens of E4M3 against 25600 rows of 6144 take 39-42 us, 34 with every load and
+// 256 tokens of E4M3 against 25600 rows of 6144 take 38-42 us, 34 with every load and
 // LDS read left out (launch, ends and MFMAs: the matrix units are busy 45 % of the 200
-// CUs' cycles, and barriers and issue take the rest); E2M1 31, 22 without loads and
+// CUs' cycles, and barriers and issue take the rest); E2M1 28-31, 22 without loads and
 // reads, 28 without the weight's stream alone. 1 token takes 15 us, 5.6 TB/s.
 template <int EF, int NI>
 struct SkinnyCfg {
@@ -531,7 +542,9 @@ void mx4_skinny_kernel(Mx4Operands op, uint16_t *__restrict__ kv, int tiles_n) {
     }                                                                                          \
   }
 // The steps behind the last whole unrolling stand apart: branches around steps of the
-// main loop made the compiler wait for every load at each of them.
+// main loop made the compiler wait for every load at each of them, as it does here (47
+// steps of which 11 stand apart against 48: 256 tokens of E4M3 38.2 us against 37.5, of E2M1
+// 30.7 against 28.4, 1 token 14.9 against 15.0).
 #define MK_LAST(u)           \
   if (kt + (u) >= KT) break; \
   MK_STEP(u, true)
@@ -608,7 +621,7 @@ hipError_t launch_skinny(const Mx4Operands &op, uint16_t *kv, hipStream_t stream
 // few tokens, multiplies padding (us, E4M3, 6144 inputs: 1 token x 25600 columns 20, 15,
 // 20, 34 with tiles of 64 x 64, 64 x 128, 128 x 128, 128 x 256 tokens x rows; 100 x 5120
 // 11, 11, 18, 31; 600 x 5120 41, 29, 22, 36). Where no such tile fits, the blocks come in
-// rounds, a round of whole 256 x 256 tiles as long as 1.6 to 1.9 of 128 x 256: those are taken
+// rounds, a round of whole 256 x 256 tiles as long as 1.4 to 1.8 of 128 x 256: those are taken
 // where their rounds number up to 5 / 3 of the whole tiles' (us, E4M3 and E2M1, 128 x 256
 // against 256 x 256; 1 round: 240 blocks of 300 x 20480, E4M3 42, 64; 2 to 2: 600 x 25600
 // 83, 126 and 63, 85; 3 to 2: 768 x 25600 115, 135 and 86, 91; 2 to 1: 256 x 33024 76, 67

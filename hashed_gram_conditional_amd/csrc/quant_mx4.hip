@@ -14,7 +14,9 @@
 // codes out), four neighbouring threads a block, which exchange their maxima
 // within the quad; 64 threads read 1 or 2 KB in a row. One group a thread: two in
 // flight took 254 us for 237 at 25600 x 6144 fp32 with values (1.34 GB, 5.7 TB/s), and
-// 8.4 for 5.9 at 4093 x 1001 bf16.
+// 8.4 for 5.9 at 4093 x 1001 bf16. Codes and scales alone take 122 us (0.71 GB, 5.9
+// TB/s), from bf16 70. A stride that is not a multiple of 8 moves value by value: 25600 x
+// 6143 fp32 takes 266 us, 605 with values.
 #include "common.h"
 #include "fast_div.h"
 

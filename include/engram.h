@@ -690,9 +690,10 @@ int engram_embed(const engram_embed_desc *desc, const void *table, const int64_t
 
 /*
  * Gradient of engram_embed with respect to the table, by sorted row ids: for every
- * row r that an id names, sum_{i: row_ids[i] = r} scale * d_out[i], summed in fp32 in
+ * row r that an id names, scale * sum_{i: row_ids[i] = r} d_out[i], summed in fp32 in
  * an order that depends on the call's sizes and ids only (no floating-point
- * atomics: the same call gives the same bits). Ids outside [0, table_rows)
+ * atomics: the same call gives the same bits), then scaled once: a row overflows
+ * where a partial sum of d_out does, whatever the scale. Ids outside [0, table_rows)
  * contribute nothing.
  *
  * engram_embed_grad: the touched rows alone, for tables whose dense gradient would
