@@ -516,3 +516,59 @@ def test_grad_run_lengths_of_longer_chunks(ot, n, dim, chunk):
     assert torch.equal(full[touched], grad[:er.size])
     full[touched] = 0
     assert (full == 0).all()
+
+
+# ---- the widest rows, the most values, special values --------------------------------
+
+@pytest.mark.parametrize("ot", [E.BF16, E.F32])
+@pytest.mark.parametrize("dim", [E.MAX_EMBED_DIM, E.MAX_EMBED_DIM - 1, 20_004, 16_392])
+def test_the_widest_rows(ot, dim):
+    """Rows of up to 32768 values: lookup, and gradients of a row named 1, 20 and 700 times."""
+    say("embed, grad: wide rows", ot, dim)
+    R, scale = 40, 1.25
+    ids = np.repeat([39, 3, 17, 0, 22], [700, 20, 1, 130, 9])
+    ids = torch.from_numpy(np.random.default_rng(dim).permutation(np.append(ids, [-1, R])).astype(np.int64))
+    n = ids.numel()
+    table = _rand((R, dim), 1, TYPES[ot])
+    got = _embed(table.to(DEV), ids.to(DEV), dim, ot, ot, scale).cpu()
+    ok = (ids >= 0) & (ids < R)
+    want = (table[ids[ok]].float() * scale).to(TYPES[ot])
+    assert torch.equal(got[ok], want) and (got[~ok] == 0).all()
+    d_out = _rand((n, dim), 2, TYPES[ot])
+    rows, grad = _check_sparse(ids, d_out, R, dim, ot, scale)
+    full = _grad(ids, d_out, R, dim, ot, scale, dense=(torch.full((R, dim), 3.0, device=DEV), 0)).cpu()
+    assert torch.equal(full[rows[:5]], grad[:5])
+
+
+def test_embed_more_values_than_one_sweep_of_threads():
+    """2.2e9 values one at a time: threads take a second turn, and the output passes 2^31."""
+    say("embed: 2.2e9 values")
+    n, dim, R = 314_600_003, 7, 1000
+    ids = torch.arange(n, device=DEV).remainder_(R + 1)          # every 1001st outside the table
+    table = _rand((R, dim), 4, torch.bfloat16).to(DEV)
+    out = torch.full((n, dim), 9.0, dtype=torch.bfloat16, device=DEV)
+    E.engram_embed(E.embed_desc(R, n, dim, E.BF16, E.BF16, 1.0), table, ids, out)
+    torch.cuda.synchronize()
+    padded = torch.cat((table, torch.zeros((1, dim), dtype=torch.bfloat16, device=DEV)))
+    for a in list(range(0, n, 40_000_000)) + [n - 5000]:
+        part = slice(a, min(n, a + 3_000_000))
+        assert torch.equal(out[part], padded[ids[part]])
+
+
+@pytest.mark.parametrize("n,dim", [(3000, 40), (3000, 7), (50_000, 24), (1_050_000, 256)])
+def test_grad_special_values_stay_in_their_row_and_column(n, dim):
+    """Infinities and NaN at kept ids reach the sums of their own row and column alone, in
+    rows named once and thousands of times."""
+    say("grad: NaN and infinity at kept ids", n, dim)
+    R = 500
+    ids = _ids(n, R, "zipf", 60, drop=0.05)
+    g = torch.Generator(device=DEV).manual_seed(n)
+    d_out = torch.empty((n, dim), device=DEV).normal_(generator=g)
+    kept = ((ids >= 0) & (ids < R)).nonzero()[:, 0]
+    spots = [(int(kept[k * len(kept) // 9]), (k * 5) % dim) for k in range(9)]
+    bad = torch.zeros((R, dim), dtype=torch.bool)
+    for k, (i, c) in enumerate(spots):
+        d_out[i, c] = (float("nan"), float("inf"), float("-inf"))[k % 3]
+        bad[ids[i], c] = True
+    full = _grad(ids, d_out, R, dim, E.F32, 0.5, dense=(torch.empty((R, dim), device=DEV), 0)).cpu()
+    assert torch.equal(~torch.isfinite(full), bad)

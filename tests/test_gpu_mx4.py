@@ -526,3 +526,68 @@ def test_project_rounds_of_tiles(fmt, tokens, K, N):
     for m in range(0, tokens, 1024):        # sums of multiples of 1/4 below 2^16: fp32 holds them
         exact = dev(ev[m:m + 1024]).float() @ wt
         assert torch.equal(got[m:m + 1024], exact.to(torch.bfloat16))
+
+
+# ---- the largest sizes, special codes -------------------------------------------------
+
+def test_quantize_more_groups_than_one_sweep_of_threads():
+    """2^28 + 12345 rows of one block: threads take a second turn, the codes pass 2^32 bytes."""
+    say("quantize: 2^28 rows")
+    rows, cols = (1 << 28) + 12345, 3
+    src = torch.arange(rows * cols, device=DEV).remainder_(251).reshape(rows, cols).to(torch.bfloat16)
+    codes = torch.full((rows, 16), 0x55, dtype=torch.uint8, device=DEV)
+    scales = torch.full((rows, 1), 0x55, dtype=torch.uint8, device=DEV)
+    E.engram_quantize_mx4(src, E.BF16, rows, cols, 0, 32, codes, scales)
+    torch.cuda.synchronize()
+    for a in (0, 70_000_000, 1 << 28, rows - 2000):
+        part = slice(a, min(rows, a + 2000))
+        ec, es, _ = quantize_reference(src[part].cpu().double().numpy(), 32)
+        assert np.array_equal(scales[part].cpu().numpy(), es) and np.array_equal(unpack(codes[part]), ec)
+
+
+@pytest.mark.parametrize("st", [E.BF16, E.F32])
+def test_quantize_the_widest_rows(st):
+    say("quantize: 2^20 columns", st)
+    cols = (1 << 20) - 5
+    x = torch.randn((3, cols + 8), generator=torch.Generator().manual_seed(7)).to(TYPES[st])
+    check_quantize(x, cols, cols + 8, 1 << 20)
+
+
+@pytest.mark.parametrize("fmt", [E.MX_E4M3, E.MX_E2M1])
+@pytest.mark.parametrize("tokens,K,N", [(1, 1 << 20, 8), (130, 1 << 20, 264), (130, (1 << 20) - 128, 264),
+                                        (2049, 1 << 20, 4104)])
+def test_project_the_longest_sums(fmt, tokens, K, N):
+    """2^20 inputs, one in 64 of them not zero: sums of small integers, exact."""
+    say("project: long sums", fmt, tokens, K, N)
+    g = torch.Generator(device=DEV).manual_seed(K + tokens)
+
+    def codes(rows, e4m3):
+        pick = torch.randint(0, 64, (rows, K), dtype=torch.uint8, device=DEV, generator=g)
+        c = torch.tensor([0x38, 0x40, 0xB8, 0xC0] if e4m3 else [2, 4, 10, 12], dtype=torch.uint8, device=DEV)
+        c = torch.where(pick < 4, c[(pick & 3).int()], 0)
+        v = torch.tensor([1.0, 2.0, -1.0, -2.0], device=DEV)
+        v = torch.where(pick < 4, v[(pick & 3).int()], 0.0)
+        return (c if e4m3 else (c[:, 0::2] | (c[:, 1::2] << 4)).contiguous()), v
+
+    e, ev = codes(tokens, fmt == E.MX_E4M3)
+    w, wv = codes(N, False)
+    es = torch.full((tokens, K // 32), 127, dtype=torch.uint8, device=DEV)
+    ws = torch.full((N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    got = project(e, es, fmt, w, ws, tokens, K, N)
+    exact = ev @ wv.t().contiguous()
+    assert exact.abs().max() > 8 and torch.equal(got, exact.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("tokens,K,N", [(3, 384, 40), (130, 896, 264), (600, 384, 25608), (2100, 640, 4104)])
+def test_project_nan_codes_stay_in_their_token(tokens, K, N):
+    """An E4M3 NaN among a token's inputs makes its outputs NaN and no other's, a zero weight
+    beside it or not; in the first input and in the last."""
+    say("project: NaN codes", tokens, K, N)
+    e, es, _ = operand(tokens, K, E.MX_E4M3, 51)
+    w, ws, _ = operand(N, K, E.MX_E2M1, 52)
+    e[1, 0], e[tokens - 1, K - 1] = 0x7F, 0xFF
+    w[:N // 2, 0] = 0
+    got = project(dev(e), dev(es), E.MX_E4M3, dev(w), dev(ws), tokens, K, N).cpu()
+    bad = torch.zeros((tokens, N), dtype=torch.bool)
+    bad[[1, tokens - 1]] = True
+    assert torch.equal(torch.isnan(got), bad)
