@@ -31,6 +31,10 @@ BF16 = 0
 F32 = 1
 MX_E4M3 = 0
 MX_E2M1 = 1
+I8 = 2
+SCALE_F32 = 0
+SCALE_POW2 = 1
+MAX_I8_IN_DIM = 131056
 MAX_EMBED_DIM = 32768
 MAX_EMBED_GRAD_IDS = 1 << 28
 
@@ -106,6 +110,17 @@ class EmbedDesc(ctypes.Structure):
     ]
 
 
+class GateSaved(ctypes.Structure):
+    _fields_ = [
+        ("kv", ctypes.c_void_p),
+        ("kv_scales", ctypes.c_void_p),
+        ("h", ctypes.c_void_p),
+        ("h_scales", ctypes.c_void_p),
+        ("kv_type", ctypes.c_int32),
+        ("h_type", ctypes.c_int32),
+    ]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(f"{_LIB_PATH} is not built; run __graft_entry__.build() "
@@ -167,6 +182,14 @@ def _load():
         "engram_quantize_mx4": (ctypes.c_int, [P, I32, I64, I64, I64, I64, P, P, P, P]),
         "engram_project_mx4": (ctypes.c_int, [P, P, I32, P, P, P, I64, I64, I64, P, SZ, P]),
         "engram_project_mx4_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "engram_sizeof_gate_saved": (SZ, []),
+        "engram_quantize_i8": (ctypes.c_int, [P, I32, I64, I64, I64, I64, I32, P, P, P, P]),
+        "engram_project_i8": (ctypes.c_int, [P, P, P, P, P, I32, I64, I64, I64, P, SZ, P]),
+        "engram_project_i8_workspace_size": (SZ, [I64, I64, I64]),
+        "engram_gate_grad_workspace_size": (SZ, [P]),
+        "engram_gate_grad": (ctypes.c_int, [P, P, I32, P, P, P, P, P, P, P, P, I32, P, SZ, P]),
+        "engram_project_grad": (ctypes.c_int, [P, P, P, P, I32, I32, I64, I64, I64, P, SZ, P]),
+        "engram_project_grad_workspace_size": (SZ, [I64, I64, I64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -180,6 +203,8 @@ def _load():
         raise ImportError("engram_short_conv layout mismatch between binding and library")
     if lib.engram_sizeof_embed_desc() != ctypes.sizeof(EmbedDesc):
         raise ImportError("engram_embed_desc layout mismatch between binding and library")
+    if lib.engram_sizeof_gate_saved() != ctypes.sizeof(GateSaved):
+        raise ImportError("engram_gate_saved layout mismatch between binding and library")
     return lib
 
 
@@ -289,6 +314,14 @@ def embed_desc(table_rows: int, n_ids: int, dim: int, table_type: int = BF16,
     d.table_rows, d.n_ids, d.table_ld, d.out_ld = table_rows, n_ids, table_ld, out_ld
     d.dim, d.table_type, d.out_type, d.scale = dim, table_type, out_type, scale
     return d
+
+
+def gate_saved(kv, kv_type: int, kv_scales, h, h_type: int, h_scales) -> GateSaved:
+    """What engram_gate_grad computes from; tensors are kept by the caller."""
+    g = GateSaved()
+    g.kv, g.kv_scales, g.kv_type = _ptr(kv), _ptr(kv_scales), kv_type
+    g.h, g.h_scales, g.h_type = _ptr(h), _ptr(h_scales), h_type
+    return g
 
 
 def engram_make_primes(base: int, count: int):
@@ -547,3 +580,53 @@ def engram_project_mx4(e_codes, e_scales, e_format: int, w_codes, w_scales, kv, 
                                   _ptr(w_scales), _ptr(kv), tokens, in_dim, out_dim,
                                   _ptr(workspace), workspace_bytes, _stream(stream, kv)),
            "engram_project_mx4")
+
+
+def engram_quantize_i8(src, src_type: int, rows: int, cols: int, src_ld: int, out_cols: int,
+                       scale_kind: int, codes, scales, values=None, stream=None):
+    """8-bit codes and one scale per row of src (and the values they stand for)."""
+    _check(LIB.engram_quantize_i8(_ptr(src), src_type, rows, cols, src_ld, out_cols, scale_kind,
+                                  _ptr(codes), _ptr(scales), _ptr(values), _stream(stream, codes)),
+           "engram_quantize_i8")
+
+
+def engram_project_i8_workspace_size(tokens: int, in_dim: int, out_dim: int) -> int:
+    return int(LIB.engram_project_i8_workspace_size(tokens, in_dim, out_dim))
+
+
+def engram_project_i8(e_codes, e_scales, w_codes, w_scales, kv, kv_type: int, tokens: int,
+                      in_dim: int, out_dim: int, workspace=None, workspace_bytes: int = 0,
+                      stream=None):
+    """The projection of 8-bit codes, scaled per token and per output channel."""
+    _check(LIB.engram_project_i8(_ptr(e_codes), _ptr(e_scales), _ptr(w_codes), _ptr(w_scales),
+                                 _ptr(kv), kv_type, tokens, in_dim, out_dim, _ptr(workspace),
+                                 workspace_bytes, _stream(stream, kv)), "engram_project_i8")
+
+
+def engram_gate_grad_workspace_size(desc: ForwardDesc) -> int:
+    return int(LIB.engram_gate_grad_workspace_size(ctypes.byref(desc)))
+
+
+def engram_gate_grad(desc: ForwardDesc, ids, raw_vocab: int, saved: GateSaved, q_w, k_w, d_out,
+                     d_h, d_kv, d_q_w, d_k_w, accumulate: int, workspace, workspace_bytes: int,
+                     stream=None):
+    """Gradients of the gate and residual update: streams, keys and value, learned scales
+    (overwritten, 0, or added to, 1)."""
+    _check(LIB.engram_gate_grad(ctypes.byref(desc), _ptr(ids), raw_vocab, ctypes.byref(saved),
+                                _ptr(q_w), _ptr(k_w), _ptr(d_out), _ptr(d_h), _ptr(d_kv),
+                                _ptr(d_q_w), _ptr(d_k_w), accumulate, _ptr(workspace),
+                                workspace_bytes, _stream(stream, d_h)), "engram_gate_grad")
+
+
+def engram_project_grad_workspace_size(tokens: int, in_dim: int, out_dim: int) -> int:
+    return int(LIB.engram_project_grad_workspace_size(tokens, in_dim, out_dim))
+
+
+def engram_project_grad(d_kv, e_codes, e_scales, grad, grad_type: int, accumulate: int,
+                        tokens: int, in_dim: int, out_dim: int, workspace=None,
+                        workspace_bytes: int = 0, stream=None):
+    """The projection weight's gradient from 8-bit codes of its inputs, overwritten (0) or
+    added to (1)."""
+    _check(LIB.engram_project_grad(_ptr(d_kv), _ptr(e_codes), _ptr(e_scales), _ptr(grad), grad_type,
+                                   accumulate, tokens, in_dim, out_dim, _ptr(workspace),
+                                   workspace_bytes, _stream(stream, grad)), "engram_project_grad")

@@ -11,7 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = ["hash.hip", "gather.hip", "hash_gather.hip", "gemm.hip", "gemm_mx.hip", "gate.hip",
            "conv.hip", "layout.hip", "embed.hip", "embed_grad.hip", "quant_mx4.hip",
-           "gemm_mx4.hip", "engram_api.hip"]
+           "gemm_mx4.hip", "quant_i8.hip", "gemm_i8.hip", "gemm_grad.hip", "gate_grad.hip",
+           "engram_api.hip"]
 LIB = os.path.join(PKG, "libengram.so")
 CALIB_SOURCE = "calibrate.hip"
 CALIB_LIB = os.path.join(PKG, "libengram_calibrate.so")

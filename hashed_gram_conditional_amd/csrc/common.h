@@ -180,4 +180,19 @@ struct EngramEmbedArgs {
   float scale;
 };
 
+// The gate's gradient (gate_grad.hip): saved inputs, gradients in and out.
+struct EngramGateGrad {
+  const int32_t *ids;
+  EngramDeadRule dead_rule;
+  const void *kv, *h;                  // saved; codes with scales, or in the I/O type
+  const float *kv_scales, *h_scales;
+  int kv_i8, h_i8, f32;
+  const float *q_w, *k_w;
+  const void *d_out;
+  void *d_h, *d_kv;
+  float *d_q_w, *d_k_w;                // both or neither
+  int accumulate;
+  float *workspace;
+};
+
 #include "launchers.h"

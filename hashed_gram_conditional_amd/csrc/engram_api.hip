@@ -329,6 +329,15 @@ int make_embed_grad_args(const engram_embed_desc *d, bool dense, EngramEmbedArgs
   return ENGRAM_OK;
 }
 
+// Shapes of the 8-bit products: 16-byte rows of codes, sums of in_dim products of at most
+// 2^14 below 2^31, and the tile bound of the bf16 projection.
+bool i8_product_shape_ok(int64_t tokens, int64_t in_dim, int64_t out_dim) {
+  if (tokens < 0 || tokens > INT32_MAX || in_dim < 16 || in_dim % 16 != 0 ||
+      in_dim > ENGRAM_MAX_I8_IN_DIM || out_dim < 8 || out_dim % 8 != 0 || out_dim > INT32_MAX)
+    return false;
+  return bf16_projection_shape_ok(tokens, in_dim, out_dim);
+}
+
 // The last HIP error an entry point returned ENGRAM_EHIP for, per host thread.
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
@@ -367,6 +376,8 @@ size_t engram_sizeof_forward_desc(void) { return sizeof(engram_forward_desc); }
 size_t engram_sizeof_short_conv(void) { return sizeof(engram_short_conv); }
 
 size_t engram_sizeof_embed_desc(void) { return sizeof(engram_embed_desc); }
+
+size_t engram_sizeof_gate_saved(void) { return sizeof(engram_gate_saved); }
 
 int engram_make_primes(int64_t base, int32_t count, int64_t *primes_out, int64_t *offsets_out,
                        int64_t *total_rows_out) {
@@ -1256,6 +1267,139 @@ int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_form
                                            (const uint8_t *)e_codes, (const uint8_t *)e_scales,
                                            e_format == ENGRAM_MX_E2M1, (uint16_t *)kv, tokens,
                                            out_dim, in_dim, stream));
+}
+
+int engram_quantize_i8(const void *src, int32_t src_type, int64_t rows, int64_t cols,
+                       int64_t src_ld, int64_t out_cols, int32_t scale_kind, void *codes,
+                       float *scales, void *values, hipStream_t stream) {
+  if (!float_type_ok(src_type)) return ENGRAM_EINVAL;
+  if (scale_kind != ENGRAM_SCALE_F32 && scale_kind != ENGRAM_SCALE_POW2) return ENGRAM_EINVAL;
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || out_cols < cols || out_cols % 16 != 0 ||
+      out_cols > ((int64_t)1 << 20))
+    return ENGRAM_ESHAPE;
+  if (rows > ((int64_t)1 << 40) / out_cols) return ENGRAM_ESHAPE;
+  if (src_ld == 0) src_ld = cols;
+  if (src_ld < cols || src_ld > INT32_MAX) return ENGRAM_ESHAPE;
+  if (rows == 0) return ENGRAM_OK;
+  if (src == nullptr || codes == nullptr || scales == nullptr) return ENGRAM_EINVAL;
+  if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(values, 16))
+    return ENGRAM_EINVAL;
+  return hip_status(engram_launch_quantize_i8(src_type == ENGRAM_F32, scale_kind == ENGRAM_SCALE_POW2,
+                                              src, rows, cols, src_ld, out_cols, (int8_t *)codes,
+                                              scales, values, stream));
+}
+
+size_t engram_project_i8_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim) {
+  (void)tokens;
+  (void)in_dim;
+  (void)out_dim;
+  return 0;
+}
+
+int engram_project_i8(const void *e_codes, const float *e_scales, const void *w_codes,
+                      const float *w_scales, void *kv, int32_t kv_type, int64_t tokens,
+                      int64_t in_dim, int64_t out_dim, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  if (!float_type_ok(kv_type)) return ENGRAM_EINVAL;
+  if (!i8_product_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
+  if (tokens == 0) return ENGRAM_OK;
+  if (e_codes == nullptr || e_scales == nullptr || w_codes == nullptr || w_scales == nullptr ||
+      kv == nullptr)
+    return ENGRAM_EINVAL;
+  if (!aligned(e_codes, 16) || !aligned(e_scales, 16) || !aligned(w_codes, 16) ||
+      !aligned(w_scales, 16) || !aligned(kv, 16))
+    return ENGRAM_EINVAL;
+  (void)workspace_bytes;
+  if (!aligned(workspace, 256)) return ENGRAM_EWORKSPACE;
+  return hip_status(engram_launch_gemm_i8((const int8_t *)w_codes, w_scales, (const int8_t *)e_codes,
+                                          e_scales, kv_type == ENGRAM_F32, kv, tokens, out_dim,
+                                          in_dim, stream));
+}
+
+size_t engram_gate_grad_workspace_size(const engram_forward_desc *desc) {
+  if (check_desc(desc) != ENGRAM_OK) return 0;
+  return engram_gate_grad_workspace(desc->batch * desc->seq, desc->hc, desc->dim);
+}
+
+int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_t raw_vocab,
+                     const engram_gate_saved *saved, const float *q_w, const float *k_w,
+                     const void *d_out, void *d_h, void *d_kv, float *d_q_w, float *d_k_w,
+                     int32_t accumulate, void *workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
+  const int rc = check_desc(desc);
+  if (rc != ENGRAM_OK) return rc;
+  if (raw_vocab < 1 || saved == nullptr) return ENGRAM_EINVAL;
+  if (accumulate != 0 && accumulate != 1) return ENGRAM_EINVAL;
+  const int own = desc->row_format == ENGRAM_ROW_F32 ? ENGRAM_F32 : ENGRAM_BF16;
+  if ((saved->kv_type != own && saved->kv_type != ENGRAM_I8) ||
+      (saved->h_type != own && saved->h_type != ENGRAM_I8))
+    return ENGRAM_EINVAL;
+  const bool kv_i8 = saved->kv_type == ENGRAM_I8, h_i8 = saved->h_type == ENGRAM_I8;
+  if ((d_q_w == nullptr) != (d_k_w == nullptr)) return ENGRAM_EINVAL;
+  if (!aligned(q_w, 16) || !aligned(k_w, 16) || !aligned(d_q_w, 16) || !aligned(d_k_w, 16))
+    return ENGRAM_EINVAL;
+  if (q_w == nullptr || k_w == nullptr) return ENGRAM_EINVAL;
+  const int64_t ntok = desc->batch * desc->seq;
+  if (ntok > 0) {
+    if (ids == nullptr || saved->kv == nullptr || saved->h == nullptr || d_out == nullptr ||
+        d_h == nullptr || d_kv == nullptr || (kv_i8 && saved->kv_scales == nullptr) ||
+        (h_i8 && saved->h_scales == nullptr))
+      return ENGRAM_EINVAL;
+    if (!aligned(ids, 4) || !aligned(saved->kv, 16) || !aligned(saved->h, 16) ||
+        !aligned(saved->kv_scales, 4) || !aligned(saved->h_scales, 4) || !aligned(d_out, 16) ||
+        !aligned(d_h, 16) || !aligned(d_kv, 16))
+      return ENGRAM_EINVAL;
+    if (d_q_w != nullptr &&
+        (workspace == nullptr || !aligned(workspace, 256) ||
+         workspace_bytes < engram_gate_grad_workspace(ntok, desc->hc, desc->dim)))
+      return ENGRAM_EWORKSPACE;
+  }
+  EngramGateGrad g;
+  g.ids = ids;
+  g.dead_rule = raw_id_rule(raw_vocab);
+  g.kv = saved->kv;
+  g.h = saved->h;
+  g.kv_scales = saved->kv_scales;
+  g.h_scales = saved->h_scales;
+  g.kv_i8 = kv_i8;
+  g.h_i8 = h_i8;
+  g.f32 = own == ENGRAM_F32;
+  g.q_w = q_w;
+  g.k_w = k_w;
+  g.d_out = d_out;
+  g.d_h = d_h;
+  g.d_kv = d_kv;
+  g.d_q_w = d_q_w;
+  g.d_k_w = d_k_w;
+  g.accumulate = accumulate;
+  g.workspace = (float *)workspace;
+  return hip_status(engram_launch_gate_grad(g, ntok, desc->hc, desc->dim, desc->eps,
+                                            desc->gate_clamp, desc->gate_mode, stream));
+}
+
+size_t engram_project_grad_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim) {
+  (void)tokens;
+  (void)in_dim;
+  (void)out_dim;
+  return 0;
+}
+
+int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_scales, void *grad,
+                        int32_t grad_type, int32_t accumulate, int64_t tokens, int64_t in_dim,
+                        int64_t out_dim, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+  if (!float_type_ok(grad_type) || (accumulate != 0 && accumulate != 1)) return ENGRAM_EINVAL;
+  if (!i8_product_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
+  if (tokens == 0 && accumulate) return ENGRAM_OK;
+  if (grad == nullptr || (tokens > 0 && (d_kv == nullptr || e_codes == nullptr || e_scales == nullptr)))
+    return ENGRAM_EINVAL;
+  if (!aligned(d_kv, 16) || !aligned(e_codes, 16) || !aligned(e_scales, 16) || !aligned(grad, 16))
+    return ENGRAM_EINVAL;
+  (void)workspace_bytes;
+  if (!aligned(workspace, 256)) return ENGRAM_EWORKSPACE;
+  return hip_status(engram_launch_gemm_grad((const uint16_t *)d_kv, (const int8_t *)e_codes, e_scales,
+                                            grad_type == ENGRAM_F32, grad, accumulate, tokens,
+                                            out_dim, in_dim, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,271 @@
+// Gradient of step 5 (gate.hip) from the streams and the keys and value it was computed
+// from, each as they were or as 8-bit codes with one scale per row. Per token t, with d =
+// d_out the gradient of the updated streams h' = h + alpha v:
+//
+//   w = q_w k_w, D = sum h w k, rh = (mean h^2 + eps)^(-1/2), rk of k,
+//   s = D rh rk / sqrt(dim), alpha = sigmoid(z), z = sign(s) sqrt(max(|s|, c)) or s
+//   c1 = (sum d v) alpha (1 - alpha) z'(s) rh rk / sqrt(dim),
+//        z' = 1 / (2 sqrt|s|) where |s| > c, else 0; or 1
+//   dh = d + c1 (k w - (D rh^2 / dim) h),  dk = c1 (h w - (D rk^2 / dim) k)
+//   dv = sum over the streams of alpha d,  dw = sum over the tokens of c1 h k,
+//   dq_w = k_w dw,  dk_w = q_w dw;  at a DEAD position dh = d, dk = dv = 0, no dw
+//
+// z' has a pole at s = 0, where D's terms cancel: D is summed in 64 bits from exact
+// products of h and k, and w = q_w k_w enters it as the product and its rounding error, so
+// that s keeps its relative precision there. Everything else is fp32.
+//
+// A block walks the tokens blockIdx.x, blockIdx.x + gridDim.x, ...; a thread owns 8 columns
+// of every stream and keeps its part of dw in registers over all of them. The blocks' parts
+// are summed by a second launch in a fixed order.
+#include "common.h"
+
+namespace {
+
+constexpr int kMaxHc = 8;
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxBlocks = 512;
+
+struct GateGradArgs {
+  const int32_t *ids;
+  EngramDeadRule dead_rule;
+  const void *kv, *h;
+  const float *kv_scales, *h_scales;   // of codes
+  const float *q_w, *k_w;
+  const void *d_out;
+  void *d_h, *d_kv;
+  float *part;                         // [gridDim.x, hc, dim], or NULL
+  int tokens, hc, dim;
+  float eps, clamp;
+  int plain;
+};
+
+// Eight consecutive saved values: a chunk of floats, or 8 codes.
+template <bool I8, bool F32>
+struct Saved8 {
+  engram::Chunk8<F32> c;
+  __device__ __forceinline__ void load(const void *p, int64_t row, int dim, int ci) {
+    c.load_nt(p, row * (dim / 8) + ci);
+  }
+  __device__ __forceinline__ float operator[](int e) const { return c[e]; }
+};
+template <bool F32>
+struct Saved8<true, F32> {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const void *p, int64_t row, int dim, int ci) {
+    const uint64_t v = __builtin_nontemporal_load(reinterpret_cast<const uint64_t *>(p) +
+                                                  row * ((dim + 15) / 16 * 2) + ci);
+    w[0] = (uint32_t)v;
+    w[1] = (uint32_t)(v >> 32);
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    return (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
+  }
+};
+
+__device__ __forceinline__ double warp_sum_d(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, engram::kWave);
+  return v;
+}
+
+// F32: fp32 streams, else bf16. KI8, HI8: keys and value, streams as codes.
+template <bool F32, bool KI8, bool HI8, int HC>
+__global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) {
+  __shared__ double red_d[2][kMaxThreads / 64];
+  __shared__ float red[2][kMaxThreads / 64][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nwaves = blockDim.x >> 6;
+  const int cps = a.dim / 8;
+  const bool on = tid < cps;
+  const int ci = on ? tid : 0;
+  const float inv_d = 1.f / (float)a.dim, inv_sqrt_d = 1.f / sqrtf((float)a.dim);
+  float dw[HC][8];
+#pragma unroll
+  for (int m = 0; m < HC; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[m][e] = 0.f;
+  int slot = 0;
+  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const bool dead = engram_dead(a.dead_rule, a.ids[t]);
+    engram::Chunk8<F32> d;
+    if (dead) {
+      if (on) {
+        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int m = 0; m <= a.hc; ++m)
+          engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, zero);
+        if (a.d_h != a.d_out)
+          for (int m = 0; m < a.hc; ++m) {
+            d.load_nt(a.d_out, (t * a.hc + m) * cps + ci);
+            d.put(a.d_h, (t * a.hc + m) * cps + ci);
+          }
+      }
+      continue;
+    }
+    Saved8<KI8, F32> v;
+    v.load(a.kv, t * (a.hc + 1) + a.hc, a.dim, ci);
+    const float sv = KI8 ? a.kv_scales[t * (a.hc + 1) + a.hc] : 1.f;
+    float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < HC; ++m) {
+      if (m >= a.hc) break;
+      Saved8<HI8, F32> h;
+      Saved8<KI8, F32> k;
+      h.load(a.h, t * a.hc + m, a.dim, ci);
+      k.load(a.kv, t * (a.hc + 1) + m, a.dim, ci);
+      d.load_nt(a.d_out, (t * a.hc + m) * cps + ci);
+      const float sh = HI8 ? a.h_scales[t * a.hc + m] : 1.f;
+      const float sk = KI8 ? a.kv_scales[t * (a.hc + 1) + m] : 1.f;
+      engram::Chunk8<true> q, kw;
+      q.load(a.q_w, (int64_t)m * cps + ci);
+      kw.load(a.k_w, (int64_t)m * cps + ci);
+      float shh = 0.f, skk = 0.f, sdv = 0.f;
+      double dot = 0.0;
+      if (on) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          shh = fmaf(h[e], h[e], shh);
+          skk = fmaf(k[e], k[e], skk);
+          sdv = fmaf(d[e], v[e], sdv);
+          dot = fma((double)h[e] * (double)k[e], (double)q[e] * (double)kw[e], dot);
+        }
+      }
+      shh = engram::warp_sum(shh);
+      skk = engram::warp_sum(skk);
+      sdv = engram::warp_sum(sdv);
+      dot = warp_sum_d(dot);
+      if (lane == 0) {
+        red[slot][wave][0] = shh;
+        red[slot][wave][1] = skk;
+        red[slot][wave][2] = sdv;
+        red_d[slot][wave] = dot;
+      }
+      __syncthreads();
+      shh = skk = sdv = 0.f;
+      dot = 0.0;
+      for (int w = 0; w < nwaves; ++w) {
+        shh += red[slot][w][0];
+        skk += red[slot][w][1];
+        sdv += red[slot][w][2];
+        dot += red_d[slot][w];
+      }
+      slot ^= 1;
+      const float rh = 1.f / sqrtf(shh * sh * sh * inv_d + a.eps);
+      const float rk = 1.f / sqrtf(skk * sk * sk * inv_d + a.eps);
+      const float D = (float)(dot * (double)sh * (double)sk);
+      const float norm = rh * rk * inv_sqrt_d;
+      const float s = D * norm;
+      const float root = sqrtf(fmaxf(fabsf(s), a.clamp));
+      const float z = a.plain ? s : copysignf(root, s);
+      const float small = expf(-fabsf(z));
+      const float alpha = (z < 0.f ? small : 1.f) / (1.f + small);
+      float slope = small / ((1.f + small) * (1.f + small));
+      if (!a.plain) slope = fabsf(s) > a.clamp ? slope / (2.f * root) : 0.f;
+      const float c1 = sdv * sv * slope * norm;
+      const float ch = c1 * sh, ck = c1 * sk;
+      const float Bh = D * rh * rh * inv_d * ch, Bk = D * rk * rk * inv_d * ck;
+      if (on) {
+        float dh[8], dk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = q[e] * kw[e];
+          dh[e] = d[e] + (ck * (k[e] * w) - Bh * h[e]);
+          dk[e] = ch * (h[e] * w) - Bk * k[e];
+          dv[e] = fmaf(alpha, d[e], dv[e]);
+          dw[m][e] = fmaf(ch * sk, h[e] * k[e], dw[m][e]);
+        }
+        engram::Chunk8<F32>::store_nt(a.d_h, (t * a.hc + m) * cps + ci, dh);
+        engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, dk);
+      }
+    }
+    if (on) engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + a.hc) * cps + ci, dv);
+  }
+  if (a.part != nullptr && on) {
+#pragma unroll
+    for (int m = 0; m < HC; ++m) {
+      if (m >= a.hc) break;
+      engram::Chunk8<true>::store(a.part, ((int64_t)blockIdx.x * a.hc + m) * cps + ci, dw[m]);
+    }
+  }
+}
+
+constexpr int kSumGroups = 4;
+
+// dq_w and dk_w of 64 columns a block: four waves sum every fourth block's part.
+__global__ __launch_bounds__(64 * kSumGroups) void gate_grad_weights_kernel(
+    const float *__restrict__ part, int blocks, int n, const float *__restrict__ q_w,
+    const float *__restrict__ k_w, float *__restrict__ d_q_w, float *__restrict__ d_k_w,
+    int accumulate) {
+  __shared__ float red[kSumGroups][64];
+  const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float sum = 0.f;
+  if (col < n)
+    for (int b = group; b < blocks; b += kSumGroups) sum += part[(int64_t)b * n + col];
+  red[group][lane] = sum;
+  __syncthreads();
+  if (group != 0 || col >= n) return;
+#pragma unroll
+  for (int g = 1; g < kSumGroups; ++g) sum += red[g][lane];
+  const float q = sum * k_w[col], k = sum * q_w[col];
+  d_q_w[col] = accumulate ? d_q_w[col] + q : q;
+  d_k_w[col] = accumulate ? d_k_w[col] + k : k;
+}
+
+int grad_blocks(int64_t tokens) { return (int)(tokens < kMaxBlocks ? tokens : kMaxBlocks); }
+
+template <bool F32, bool KI8, bool HI8>
+void launch(const GateGradArgs &a, int blocks, int threads, hipStream_t stream) {
+  if (a.hc <= 4)
+    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8, 4>), dim3(blocks), dim3(threads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8, 8>), dim3(blocks), dim3(threads), 0, stream, a);
+}
+
+}  // namespace
+
+size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim) {
+  return (size_t)grad_blocks(tokens) * hc * dim * sizeof(float);
+}
+
+hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
+                                   float eps, float clamp, int plain, hipStream_t stream) {
+  GateGradArgs a;
+  a.ids = g.ids;
+  a.dead_rule = g.dead_rule;
+  a.kv = g.kv;
+  a.h = g.h;
+  a.kv_scales = g.kv_scales;
+  a.h_scales = g.h_scales;
+  a.q_w = g.q_w;
+  a.k_w = g.k_w;
+  a.d_out = g.d_out;
+  a.d_h = g.d_h;
+  a.d_kv = g.d_kv;
+  a.part = g.d_q_w != nullptr ? g.workspace : nullptr;
+  a.tokens = (int)tokens;
+  a.hc = hc;
+  a.dim = dim;
+  a.eps = eps;
+  a.clamp = clamp;
+  a.plain = plain;
+  const int blocks = grad_blocks(tokens), threads = (dim / 8 + 63) / 64 * 64;
+#define ENGRAM_GATE_GRAD(F)                                                 \
+  if (g.kv_i8 && g.h_i8) launch<F, true, true>(a, blocks, threads, stream); \
+  else if (g.kv_i8) launch<F, true, false>(a, blocks, threads, stream);     \
+  else if (g.h_i8) launch<F, false, true>(a, blocks, threads, stream);      \
+  else launch<F, false, false>(a, blocks, threads, stream)
+  if (tokens <= 0) {
+    a.part = g.d_q_w;      // no part is read
+  } else if (g.f32) {
+    ENGRAM_GATE_GRAD(true);
+  } else {
+    ENGRAM_GATE_GRAD(false);
+  }
+#undef ENGRAM_GATE_GRAD
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || a.part == nullptr) return err;
+  const int n = hc * dim;
+  hipLaunchKernelGGL(gate_grad_weights_kernel, dim3((n + 63) / 64), dim3(64 * kSumGroups), 0, stream,
+                     g.workspace, blocks, n, g.q_w, g.k_w, g.d_q_w, g.d_k_w, g.accumulate);
+  return hipGetLastError();
+}

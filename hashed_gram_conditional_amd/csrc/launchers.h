@@ -145,3 +145,25 @@ hipError_t engram_launch_quantize_mx4(bool f32, const void *src, int64_t rows, i
 hipError_t engram_launch_gemm_mx4(const uint8_t *w_codes, const uint8_t *w_scales,
                                   const uint8_t *e_codes, const uint8_t *e_scales, bool e_fp4,
                                   uint16_t *kv, int64_t m, int64_t n, int64_t k, hipStream_t stream);
+
+// 8-bit codes [rows, out_cols] and fp32 scales [rows] of a [rows, cols] array; values (or
+// NULL) as src.
+hipError_t engram_launch_quantize_i8(bool f32, bool pow2, const void *src, int64_t rows,
+                                     int64_t cols, int64_t ld, int64_t out_cols, int8_t *codes,
+                                     float *scales, void *values, hipStream_t stream);
+
+// Projection with 8-bit codes: W [n, k], e [m, k], one fp32 scale per row of each; kv bf16
+// or fp32 [m, n].
+hipError_t engram_launch_gemm_i8(const int8_t *w_codes, const float *w_scales, const int8_t *e_codes,
+                                 const float *e_scales, bool f32, void *kv, int64_t m, int64_t n,
+                                 int64_t k, hipStream_t stream);
+
+// The gate's gradient; the workspace holds engram_gate_grad_workspace bytes.
+size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim);
+hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
+                                   float eps, float clamp, int plain, hipStream_t stream);
+
+// The projection weight's gradient [n, k] from d_kv bf16 [t, n] and codes [t, k].
+hipError_t engram_launch_gemm_grad(const uint16_t *d_kv, const int8_t *e_codes, const float *e_scales,
+                                   bool f32, void *grad, int accumulate, int64_t t, int64_t n,
+                                   int64_t k, hipStream_t stream);

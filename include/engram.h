@@ -1,7 +1,8 @@
 /*
  * engram.h -- C ABI of the Engram conditional-memory layer forward for
  * AMD Instinct MI355X (gfx950), with the scaled lookup of a table and its
- * gradient, and the 4-bit quantiser and projection.
+ * gradient, the 4-bit quantiser and projection, and the 8-bit integer quantiser,
+ * projection and the layer's gradients from 8-bit checkpoints.
  *
  * The layer (pages cited by title, then section / equation / table):
  *   [P1] "DeepSeek-V4.1 模型结构（5）：记忆，Engram"
@@ -185,11 +186,21 @@ typedef struct engram_short_conv {
   float *state_s_out;         /*   (both NULL or both set); may equal the inputs   */
 } engram_short_conv;
 
-/* Element types of engram_embed, its gradient and engram_quantize_mx4. */
+/* Element types of engram_embed, its gradient and the quantisers, and of what
+ * engram_gate_saved holds. */
 typedef enum engram_float_type {
   ENGRAM_BF16 = 0,
-  ENGRAM_F32 = 1
+  ENGRAM_F32 = 1,
+  ENGRAM_I8 = 2               /* engram_gate_saved only: engram_quantize_i8's codes,
+                                 one fp32 scale per row                            */
 } engram_float_type;
+
+/* The scale that engram_quantize_i8 gives a row of largest magnitude amax. */
+typedef enum engram_scale_kind {
+  ENGRAM_SCALE_F32 = 0,       /* amax / 127                                        */
+  ENGRAM_SCALE_POW2 = 1       /* the smallest power of two s with amax <= 127 s: up to
+                                 twice as coarse, but a code times s is exact in bf16 */
+} engram_scale_kind;
 
 /* Element formats of engram_project_mx4's e operand; both carry one E8M0 scale
  * (2^(s - 127), 0xFF = NaN) per 32 consecutive inputs. */
@@ -216,6 +227,25 @@ typedef struct engram_embed_desc {
   float scale;                /* finite                                            */
 } engram_embed_desc;
 
+#define ENGRAM_MAX_I8_IN_DIM 131056  /* in_dim of the 8-bit products: sums below 2^31 */
+
+/*
+ * What engram_gate_grad computes from: kv and h (before the update) of
+ * engram_gate, each in the layer's own type (ENGRAM_BF16, or ENGRAM_F32 for
+ * ENGRAM_ROW_F32) or as 8-bit codes (ENGRAM_I8). The rows of codes are one key,
+ * value or stream each, dim rounded up to a multiple of 16 apart, with one scale a
+ * row: engram_quantize_i8 of [tokens * (hc+1), dim] or [tokens * hc, dim] with
+ * out_cols = that multiple.
+ */
+typedef struct engram_gate_saved {
+  const void *kv;             /* device [B*T, hc + 1, dim]                         */
+  const float *kv_scales;     /* device [B*T, hc + 1]; NULL unless kv_type is I8   */
+  const void *h;              /* device [B*T, hc, dim]                             */
+  const float *h_scales;      /* device [B*T, hc]; NULL unless h_type is I8        */
+  int32_t kv_type;            /* engram_float_type                                 */
+  int32_t h_type;
+} engram_gate_saved;
+
 /* Message for a status code (static storage). */
 const char *engram_status_string(int status);
 
@@ -229,6 +259,7 @@ size_t engram_sizeof_hash_params(void);
 size_t engram_sizeof_forward_desc(void);
 size_t engram_sizeof_short_conv(void);
 size_t engram_sizeof_embed_desc(void);
+size_t engram_sizeof_gate_saved(void);
 
 /*
  * [host] Segment sizes and offsets: the first `count` primes >= base, in
@@ -779,6 +810,112 @@ int engram_project_mx4(const void *e_codes, const void *e_scales, int32_t e_form
 /* [host] Bytes of workspace engram_project_mx4 uses (0: none, or bad arguments). */
 size_t engram_project_mx4_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim,
                                          int32_t e_format);
+
+/*
+ * Quantisation to 8-bit integers with one scale per row: for a row of largest
+ * magnitude amax the scale s of scale_kind and the codes q, x (127 / amax rounded to
+ * fp32) or x / s to the nearest whole number (ties to even), so |q| <= 127. A row with
+ * amax < 2^-119 counts as zeros and gets scale 0; a row that holds an infinity or a NaN
+ * gets scale NaN and zero codes. It serves activations (a row per token), weights (a row
+ * per output channel) and checkpoints of either.
+ *   src       src_type [rows, cols], rows src_ld elements apart (0 = cols, else
+ *             >= cols); 16-byte aligned
+ *   out_cols  columns written, a multiple of 16 and >= cols, at most 2^20; columns
+ *             from cols on get zero codes
+ *   codes     int8 [rows, out_cols], 16-byte aligned
+ *   scales    float [rows], 16-byte aligned
+ *   values    NULL, or src_type [rows, cols] with src's strides: q s, rounded once to
+ *             src_type (NaN in a NaN row); may be src itself
+ * rows <= 2^31 - 1 and rows * out_cols <= 2^40.
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EHIP.
+ */
+int engram_quantize_i8(const void *src, int32_t src_type, int64_t rows, int64_t cols,
+                       int64_t src_ld, int64_t out_cols, int32_t scale_kind, void *codes,
+                       float *scales, void *values, hipStream_t stream);
+
+/*
+ * Step 4 with 8-bit integer operands: kv[t, c] = e_scales[t] w_scales[c] sum_k e[t, k]
+ * W[c, k]. The sum is exact (32-bit integers); it is rounded to fp32, multiplied by the
+ * channel's and then by the token's scale in fp32, and rounded to kv_type.
+ *   e_codes   int8 [tokens, in_dim], 16-byte aligned; any value, -128 included
+ *   e_scales  float [tokens], 16-byte aligned
+ *   w_codes   int8 [out_dim, in_dim], 16-byte aligned
+ *   w_scales  float [out_dim], 16-byte aligned
+ *   kv        kv_type [tokens, out_dim], 16-byte aligned
+ *   in_dim    a multiple of 16, at most ENGRAM_MAX_I8_IN_DIM; out_dim % 8 == 0; the
+ *             tile bound of engram_project
+ *   workspace as for engram_project, sized by engram_project_i8_workspace_size. The
+ *             result does not depend on it
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
+ */
+int engram_project_i8(const void *e_codes, const float *e_scales, const void *w_codes,
+                      const float *w_scales, void *kv, int32_t kv_type, int64_t tokens,
+                      int64_t in_dim, int64_t out_dim, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/* [host] Bytes of workspace engram_project_i8 uses on the current device (0: none, bad
+ * arguments or a HIP error). */
+size_t engram_project_i8_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim);
+
+/*
+ * Gradient of step 5 (engram_gate): from the gradient d_out of the updated streams those
+ * of the streams before the update, of the keys and the value, and of the learned
+ * scales, at the saved point (the gate is computed anew from it):
+ *   D = sum h q_w k_w k, s = D rh rk / sqrt(dim), rh = (mean h^2 + eps)^(-1/2), rk of k,
+ *   c1 = (sum_i d_out_i v_i) alpha'(s) rh rk / sqrt(dim)
+ *   d_h = d_out + c1 (q_w k_w k - D rh^2 / dim h), d_k = c1 (q_w k_w h - D rk^2 / dim k),
+ *   d_v = sum over the streams of alpha d_out,
+ *   d_q_w = k_w sum over the tokens of c1 h k, d_k_w = q_w of the same
+ * The signed root's derivative is taken as 0 where |s| <= gate_clamp (at s = 0 with
+ * clamp 0 too). A DEAD position passes d_out on, with a zero d_kv row and no part in
+ * d_q_w and d_k_w; its saved rows are not used.
+ *   desc       as engram_gate: batch, seq, hc, dim, row_format, eps, gate_clamp, gate_mode
+ *   ids        int32 [B, T], raw_vocab: as engram_gate
+ *   saved      [host] the saved inputs
+ *   q_w, k_w   float [hc, dim]
+ *   d_out      [B*T, hc, dim], bf16 or float by row_format
+ *   d_h        as d_out; may be d_out itself
+ *   d_kv       [B*T, (hc+1) dim], as d_out; bf16 rows are engram_project_grad's operand
+ *   d_q_w, d_k_w  float [hc, dim], or both NULL; accumulate 1: added to, 0: overwritten
+ *   workspace  device, >= engram_gate_grad_workspace_size bytes, 256-byte aligned, or
+ *              NULL without d_q_w; contents are scratch
+ * No other buffers may overlap. Sums run in an order that depends on the sizes only.
+ * The gradient with respect to the inputs e is engram_project of d_kv with the
+ * transposed weight (engram_transpose), and engram_embed_grad takes that to the table.
+ * Errors: ENGRAM_EINVAL (also a saved type that is neither the layer's own nor I8),
+ * ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
+ */
+size_t engram_gate_grad_workspace_size(const engram_forward_desc *desc);
+int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_t raw_vocab,
+                     const engram_gate_saved *saved, const float *q_w, const float *k_w,
+                     const void *d_out, void *d_h, void *d_kv, float *d_q_w, float *d_k_w,
+                     int32_t accumulate, void *workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+
+/*
+ * Gradient of the projection's weight from its inputs in 8-bit codes (the operand of
+ * engram_project_i8, or a checkpoint of e): grad[c, k] = sum_t d_kv[t, c] e_scales[t]
+ * e[t, k], fp32 accumulation in the bf16 MFMA. e_scales[t] e[t, k] is rounded to bf16
+ * first, which ENGRAM_SCALE_POW2 scales make exact.
+ *   d_kv      bf16 [tokens, out_dim], 16-byte aligned
+ *   e_codes   int8 [tokens, in_dim], 16-byte aligned
+ *   e_scales  float [tokens], 16-byte aligned
+ *   grad      grad_type [out_dim, in_dim], 16-byte aligned; accumulate 1: the sums are
+ *             added to it, 0: it is overwritten (with zeros for no tokens)
+ *   in_dim, out_dim, tokens  as engram_project_i8
+ *   workspace NULL, or at least engram_project_grad_workspace_size bytes, 256-byte
+ *             aligned: calls with fewer output tiles than the GPU has CUs then split
+ *             the tokens over them, with fp32 parts summed in a fixed order
+ * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
+ */
+int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_scales, void *grad,
+                        int32_t grad_type, int32_t accumulate, int64_t tokens, int64_t in_dim,
+                        int64_t out_dim, void *workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/* [host] Bytes of workspace engram_project_grad uses on the current device (0: none, bad
+ * arguments or a HIP error). */
+size_t engram_project_grad_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim);
 
 #ifdef __cplusplus
 }
