@@ -35,6 +35,7 @@ I8 = 2
 SCALE_F32 = 0
 SCALE_POW2 = 1
 MAX_I8_IN_DIM = 131056
+MAX_GRAD_OUT_DIM = 1 << 23
 MAX_EMBED_DIM = 32768
 MAX_EMBED_GRAD_IDS = 1 << 28
 

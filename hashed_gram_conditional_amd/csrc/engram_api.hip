@@ -338,6 +338,12 @@ bool i8_product_shape_ok(int64_t tokens, int64_t in_dim, int64_t out_dim) {
   return bf16_projection_shape_ok(tokens, in_dim, out_dim);
 }
 
+// The weight's gradient also addresses 64 rows of d_kv through 32-bit byte counts and numbers
+// its 256 x 256 tiles (times their splits) and groups of 4 gradients in 32-bit grids.
+bool i8_gradient_shape_ok(int64_t tokens, int64_t in_dim, int64_t out_dim) {
+  return i8_product_shape_ok(tokens, in_dim, out_dim) && out_dim <= ENGRAM_MAX_GRAD_OUT_DIM;
+}
+
 // The last HIP error an entry point returned ENGRAM_EHIP for, per host thread.
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
@@ -1378,10 +1384,8 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
 }
 
 size_t engram_project_grad_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim) {
-  (void)tokens;
-  (void)in_dim;
-  (void)out_dim;
-  return 0;
+  if (!i8_gradient_shape_ok(tokens, in_dim, out_dim) || tokens == 0) return 0;
+  return engram_gemm_grad_workspace(tokens, out_dim, in_dim);
 }
 
 int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_scales, void *grad,
@@ -1389,17 +1393,19 @@ int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_sc
                         int64_t out_dim, void *workspace, size_t workspace_bytes,
                         hipStream_t stream) {
   if (!float_type_ok(grad_type) || (accumulate != 0 && accumulate != 1)) return ENGRAM_EINVAL;
-  if (!i8_product_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
+  if (!i8_gradient_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
   if (tokens == 0 && accumulate) return ENGRAM_OK;
   if (grad == nullptr || (tokens > 0 && (d_kv == nullptr || e_codes == nullptr || e_scales == nullptr)))
     return ENGRAM_EINVAL;
   if (!aligned(d_kv, 16) || !aligned(e_codes, 16) || !aligned(e_scales, 16) || !aligned(grad, 16))
     return ENGRAM_EINVAL;
-  (void)workspace_bytes;
-  if (!aligned(workspace, 256)) return ENGRAM_EWORKSPACE;
+  const size_t need = engram_project_grad_workspace_size(tokens, in_dim, out_dim);
+  if (workspace != nullptr && (!aligned(workspace, 256) || workspace_bytes < need))
+    return ENGRAM_EWORKSPACE;
   return hip_status(engram_launch_gemm_grad((const uint16_t *)d_kv, (const int8_t *)e_codes, e_scales,
                                             grad_type == ENGRAM_F32, grad, accumulate, tokens,
-                                            out_dim, in_dim, stream));
+                                            out_dim, in_dim,
+                                            need > 0 ? (float *)workspace : nullptr, stream));
 }
 
 }  // extern "C"
