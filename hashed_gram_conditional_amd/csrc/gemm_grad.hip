@@ -128,7 +128,7 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
 #define GR_LOAD(kt_, st)                                                                       \
   {                                                                                            \
     const int t_ = t_first + (kt_) * kStep;                                                    \
-    const int rows_ = max(0, min(kStep, t_last - t_));                                         \
+    const int rows_ = t_ >= t_last ? 0 : t_last - t_ < kStep ? t_last - t_ : kStep;            \
     const int64_t at_ = rows_ > 0 ? t_ : 0;                                                    \
     const __amdgpu_buffer_rsrc_t rsD = __builtin_amdgcn_make_buffer_rsrc(                      \
         const_cast<uint16_t *>(op.d_kv + at_ * op.N + n0), 0,                                  \
@@ -171,26 +171,38 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
 #define GR_FENCE() __builtin_amdgcn_sched_barrier(0)
+#define GR_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier(mask, n, 0)
+// 16 MFMAs, a fragment's read behind each, and between them the conversion of two rows
+#define GR_MIX()                                                                               \
+  _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                          \
+    GR_GROUP(0x008, 1); GR_GROUP(0x100, 1); GR_GROUP(0x002, 6);                                \
+    if (g_ % 4 == 3) GR_GROUP(0x200, 1);                                                       \
+  }                                                                                            \
+  GR_FENCE();
 #define GR_STEP(kt_, P, Q)                                                                     \
   {                                                                                            \
     GR_FRAGS(P, 1, fa1, fb1)                                                                   \
     GR_MFMA(fa0, fb0)                                                                          \
+    _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) { GR_GROUP(0x008, 1); GR_GROUP(0x100, 1); } \
     GR_FENCE();                                                                                \
     GR_FRAGS(P, 2, fa0, fb0)                                                                   \
     GR_WRITE(Q, 0)                                                                             \
     GR_WRITE(Q, 1)                                                                             \
     GR_MFMA(fa1, fb1)                                                                          \
-    GR_FENCE();                                                                                \
+    GR_MIX()                                                                                   \
     GR_FRAGS(P, 3, fa1, fb1)                                                                   \
     GR_WRITE(Q, 2)                                                                             \
     GR_WRITE(Q, 3)                                                                             \
     GR_MFMA(fa0, fb0)                                                                          \
-    GR_FENCE();                                                                                \
+    GR_MIX()                                                                                   \
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");                   \
     GR_FENCE();                                                                                \
     GR_FRAGS(Q, 0, fa0, fb0)                                                                   \
     GR_LOAD((kt_) + 2, P)                                                                      \
     GR_MFMA(fa1, fb1)                                                                          \
+    _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                        \
+      GR_GROUP(0x008, 1); GR_GROUP(0x100, 2); GR_GROUP(0x020, 2);                              \
+    }                                                                                          \
     GR_FENCE();                                                                                \
   }
   f32x16 acc[4][4];
@@ -220,6 +232,8 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
       store_patch<F32, ADD, F32 || ADD ? 32 : 64>(acc[i][j], acc[i + (F32 || ADD ? 0 : 1)][j], patch, grad, op.N,
                                                   op.K, n0 + wn * 128 + j * 32, k0 + wk * 128 + i * 32, lane);
 #undef GR_STEP
+#undef GR_MIX
+#undef GR_GROUP
 #undef GR_FENCE
 #undef GR_MFMA
 #undef GR_FRAGS
