@@ -1,13 +1,10 @@
 // Gradient of the projection's weight from 8-bit codes of its inputs: dW[n, k] = sum_t
-// d_kv[t, n] s_t q[t, k]. Both operands have the summed index outermost; LDS reads that
-// transpose 4 x 16 blocks (ds_read_b64_tr_b16) bring it innermost for the MFMA.
+// d_kv[t, n] s_t q[t, k]. Both operands have the summed index outermost.
 #include "gemm_tiles.h"
 
 using namespace engram_gemm;
 
 namespace {
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 struct GradOperands {
   const uint16_t *d_kv;      // [T, N] bf16
@@ -18,21 +15,8 @@ struct GradOperands {
 
 constexpr int kStep = 64;                 // tokens per step
 constexpr int kTile = 256;                // columns of either operand
-constexpr int kRow = kTile * 2;           // bytes of a row in LDS
+constexpr int kRow = kStep * 2;           // bytes of a column in LDS
 constexpr int kPatch = 4096;              // LDS of a wave for storing part of its tile
-
-__device__ __forceinline__ s16x4 read_tr(const uint8_t *p) {
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p));
-}
-
-__device__ __forceinline__ bf16x8 join(s16x4 a, s16x4 b) {
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-}
-
-// Two codes (bytes 2 i and 2 i + 1 of w's low or high half) times s, as bf16.
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t w, int i, float s) {
-  return engram::pack_bf16x2((float)(int8_t)(w >> (16 * i)) * s, (float)(int8_t)(w >> (16 * i + 8)) * s);
-}
 
 // Stores 32 rows (n) x COLS columns (k, one or two accumulators) of a wave in whole cache
 // lines, through LDS: a lane's accumulators are 4 columns of one row at a time. ADD: added
@@ -83,125 +67,147 @@ __device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, 
   }
 }
 
+// Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 4 tiles of d_kv's
+// columns by all of e's, so that its 32 blocks share 4 panels of d_kv (512 bytes a token)
+// and 8 of codes (256).
+constexpr int kGroupN = 4;
+
+__device__ __forceinline__ void grad_tile(int bid, int tiles_n, int tiles_k, int &n0, int &k0) {
+  const int full = tiles_n * tiles_k / kXcds * kXcds;
+  if (bid < full) bid = (bid % kXcds) * (full / kXcds) + bid / kXcds;
+  const int group = bid / (kGroupN * tiles_k);
+  const int size = min(tiles_n - group * kGroupN, kGroupN);
+  const int local = bid - group * kGroupN * tiles_k;
+  n0 = (group * kGroupN + local % size) * kTile;
+  k0 = local / size * kTile;
+}
+
 // A block sums the tokens [split * per, (split + 1) * per) of one 256 x 256 tile (four waves
-// of 128 x 128) in steps of 64, two stages. d_kv goes global -> LDS by direct loads; codes go
-// through registers, where they are scaled and rounded to bf16: those of step kt + 2 are
-// requested at the end of step kt and written to LDS during step kt + 1, whose stage is the
-// other one. In a row of LDS the 64-byte group of column c sits at group ^ (t % 4), so that
-// the four rows of a transposing read fall into different banks.
+// of 128 x 128) in steps of 64, two stages. LDS holds a step as the MFMA reads it, the tokens
+// innermost: column c is a row of 128 bytes, tokens 8 g .. 8 g + 7 its chunk g, in slot g ^ f(c).
+// Both operands are turned on the way through registers: a thread loads 8 columns of 8 tokens
+// of each, and pairs of neighbouring tokens meet in one byte permutation (d_kv) or in the
+// rounding of two scaled codes to bf16 (e). A register set is requested again, for the step
+// after next, as soon as it is written to LDS, so that its loads have a whole step.
 template <bool F32, bool ADD>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tiles_k,
                  int tiles, int per) {
-  __shared__ __align__(1024) uint8_t d0[kStep * kRow], d1[kStep * kRow];
-  __shared__ __align__(1024) uint8_t e0[kStep * kRow], e1[kStep * kRow];
+  __shared__ __align__(1024) uint8_t d0[kTile * kRow], d1[kTile * kRow];
+  __shared__ __align__(1024) uint8_t e0[kTile * kRow], e1[kTile * kRow];
   __shared__ __align__(1024) uint8_t out[4 * kPatch];
   const int split = (int)blockIdx.x / tiles;
   int n0, k0;
-  tile_origin_of((int)blockIdx.x - split * tiles, tiles_n, tiles_k, kTile, n0, k0);
+  grad_tile((int)blockIdx.x - split * tiles, tiles_n, tiles_k, n0, k0);
   const int t_first = split * per, t_last = min(op.T, t_first + per);
   const int steps = ((t_last - t_first + kStep - 1) / kStep + 1) & ~1;      // a step of zeros if odd
   if (gridDim.x > (unsigned)tiles) grad = reinterpret_cast<float *>(grad) + (int64_t)split * op.N * op.K;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wn = wave & 1;
-  // direct load i of a wave fills 1 KB: rows 16 wave + 2 i and the next (lane p: row p / 32,
-  // slot p % 32)
-  const int d_row = (wave * 16 + (lane >> 5)) * op.N * 2;
-  const int d_v0 = d_row + (((lane & 31) ^ (lane >> 5 << 2)) << 4);
-  const int d_v1 = d_row + (((lane & 31) ^ ((2 + (lane >> 5)) << 2)) << 4);
-  // codes: 16 threads a row of 256, four rows a thread, 16 apart
-  const int c_row = tid >> 4, c_col = tid & 15;
-  const int e_v = c_row * op.K + c_col * 16;
-  const int e_w = c_row * kRow + (((c_col * 2) ^ ((c_row & 3) << 2)) << 4);
-  // a lane's address in a 16 (t) x 32 block: row, and the bytes of its column
-  const int group = lane >> 4, in = lane & 15;
-  const int tr_row = (group >> 1) * 8 + in / 4;
-  const int tr_x = (tr_row & 3) << 6, tr_c = (group & 1) * 32 + in % 4 * 8;
-  const int a_base = tr_row * kRow + tr_c, b_base = a_base;
+  // a thread's 8 tokens (group) and 8 columns
+  const int tg = tid >> 5, tc = tid & 31;
+  const int d_v = tg * 8 * op.N * 2 + tc * 16, e_v = tg * 8 * op.K + tc * 8;
+  // f(c) = (c ^ c / 8) % 8: eight columns of a thread's, and eight threads' columns of the
+  // same number, lie in different slots
+  const int w_base = tc * 8 * kRow, w_x = tg ^ (tc & 7);
+  const int frow = lane & 31, h = lane >> 5;
+  const int a_base = (wk * 128 + frow) * kRow, b_base = (wn * 128 + frow) * kRow;
+  const int f_x = (frow ^ frow >> 3) & 7;
 #define GR_D(st) ((st) ? d1 : d0)
 #define GR_E(st) ((st) ? e1 : e0)
-  uint4 codes[4];
-  float scale[4];
-// requests step kt_: codes and scales into registers, d_kv into stage st; rows behind the
-// last token are zeros
-#define GR_LOAD(kt_, st)                                                                       \
-  {                                                                                            \
+  uint4 dv[8];
+  uint2 ev[8];
+  float4 sv[2];
+// Rows behind the last token are zeros.
+#define GR_ROWS(kt_)                                                                           \
     const int t_ = t_first + (kt_) * kStep;                                                    \
     const int rows_ = t_ >= t_last ? 0 : t_last - t_ < kStep ? t_last - t_ : kStep;            \
-    const int64_t at_ = rows_ > 0 ? t_ : 0;                                                    \
-    const __amdgpu_buffer_rsrc_t rsD = __builtin_amdgcn_make_buffer_rsrc(                      \
+    const int64_t at_ = rows_ > 0 ? t_ : 0;
+// requests d_kv of step kt_, or its codes and scales
+#define GR_LOADD(kt_)                                                                          \
+  {                                                                                            \
+    GR_ROWS(kt_)                                                                               \
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(                       \
         const_cast<uint16_t *>(op.d_kv + at_ * op.N + n0), 0,                                  \
         rows_ > 0 ? (rows_ * op.N - n0) * 2 : 0, kBufferFlags);                                \
-    const __amdgpu_buffer_rsrc_t rsE = __builtin_amdgcn_make_buffer_rsrc(                      \
+    _Pragma("unroll") for (int r = 0; r < 8; ++r) dv[r] = load16(rs, d_v, r * op.N * 2);       \
+  }
+#define GR_LOADE(kt_)                                                                          \
+  {                                                                                            \
+    GR_ROWS(kt_)                                                                               \
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(                       \
         const_cast<int8_t *>(op.e_codes + at_ * op.K + k0), 0, rows_ > 0 ? rows_ * op.K - k0 : 0, \
         kBufferFlags);                                                                         \
     const __amdgpu_buffer_rsrc_t rsS = __builtin_amdgcn_make_buffer_rsrc(                      \
         const_cast<float *>(op.e_scales + at_), 0, rows_ * 4, kBufferFlags);                   \
-    _Pragma("unroll") for (int i = 0; i < 4; ++i) {                                            \
-      codes[i] = load16(rsE, e_v, i * 16 * op.K);                                              \
-      scale[i] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsS, c_row * 4, i * 64, 0)); \
+    _Pragma("unroll") for (int r = 0; r < 8; ++r) {                                            \
+      const auto v_ = __builtin_amdgcn_raw_buffer_load_b64(rs, e_v, r * op.K, 0);              \
+      ev[r] = make_uint2((uint32_t)v_[0], (uint32_t)v_[1]);                                    \
     }                                                                                          \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds(    \
-        rsD, ENGRAM_LDS(&GR_D(st)[(wave * 8 + i) * 1024]), 16, (i & 1) ? d_v1 : d_v0,          \
-        i * 4 * op.N, 0, 0);                                                                   \
+    _Pragma("unroll") for (int r = 0; r < 2; ++r)                                              \
+      sv[r] = __builtin_bit_cast(float4, load16(rsS, tg * 32, r * 16));                        \
   }
-#define GR_WRITE(st, i)                                                                        \
-  {                                                                                            \
-    uint4 lo_, hi_;                                                                            \
-    lo_.x = scaled_pair(codes[i].x, 0, scale[i]);                                              \
-    lo_.y = scaled_pair(codes[i].x, 1, scale[i]);                                              \
-    lo_.z = scaled_pair(codes[i].y, 0, scale[i]);                                              \
-    lo_.w = scaled_pair(codes[i].y, 1, scale[i]);                                              \
-    hi_.x = scaled_pair(codes[i].z, 0, scale[i]);                                              \
-    hi_.y = scaled_pair(codes[i].z, 1, scale[i]);                                              \
-    hi_.z = scaled_pair(codes[i].w, 0, scale[i]);                                              \
-    hi_.w = scaled_pair(codes[i].w, 1, scale[i]);                                              \
-    *reinterpret_cast<uint4 *>(&GR_E(st)[e_w + (i) * 16 * kRow]) = lo_;                        \
-    *reinterpret_cast<uint4 *>(&GR_E(st)[(e_w ^ 16) + (i) * 16 * kRow]) = hi_;                 \
-  }
-// fragments of tokens 16 s .. 16 s + 15: columns wk * 128 + 32 i of e, wn * 128 + 32 j of d_kv
-#define GR_FRAG(buf, base, w, i, s)                                                            \
-  join(read_tr(&(buf)[(base) + (s) * 16 * kRow + (((w) * 256 + (i) * 64) ^ tr_x)]),            \
-       read_tr(&(buf)[(base) + ((s) * 16 + 4) * kRow + (((w) * 256 + (i) * 64) ^ tr_x)]))
+#define GR_AT(buf, j) (*reinterpret_cast<uint4 *>(&(buf)[w_base + (j) * kRow + ((w_x ^ (j)) << 4)]))
+// column j of d_kv: the low or high halves of word j / 2 of the 8 tokens, in pairs
+#define GR_WORD(v, at) ((at) == 0 ? (v).x : (at) == 1 ? (v).y : (at) == 2 ? (v).z : (v).w)
+#define GR_PAIR(r, j)                                                                          \
+  __builtin_amdgcn_perm(GR_WORD(dv[(r) + 1], (j) / 2), GR_WORD(dv[r], (j) / 2), (j) & 1 ? 0x07060302u : 0x05040100u)
+#define GR_WRITED(st)                                                                          \
+  _Pragma("unroll") for (int j = 0; j < 8; ++j)                                                \
+    GR_AT(GR_D(st), j) = make_uint4(GR_PAIR(0, j), GR_PAIR(2, j), GR_PAIR(4, j), GR_PAIR(6, j));
+// columns 4 q .. 4 q + 3 of e
+#define GR_CODE(r, q, j) ((float)(int8_t)(((q) ? ev[r].y : ev[r].x) >> (8 * (j))))
+#define GR_WRITEE(st, q)                                                                       \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j)                                                \
+    GR_AT(GR_E(st), 4 * (q) + j) = make_uint4(                                                 \
+        engram::pack_bf16x2(GR_CODE(0, q, j) * sv[0].x, GR_CODE(1, q, j) * sv[0].y),           \
+        engram::pack_bf16x2(GR_CODE(2, q, j) * sv[0].z, GR_CODE(3, q, j) * sv[0].w),           \
+        engram::pack_bf16x2(GR_CODE(4, q, j) * sv[1].x, GR_CODE(5, q, j) * sv[1].y),           \
+        engram::pack_bf16x2(GR_CODE(6, q, j) * sv[1].z, GR_CODE(7, q, j) * sv[1].w));
+// fragments s of a step: half h of a wave takes tokens 8 (4 h + s) .. + 7
+#define GR_FRAG(buf, base, i, s)                                                               \
+  (*reinterpret_cast<const bf16x8 *>(&(buf)[(base) + (i) * 32 * kRow + (((4 * h + (s)) ^ f_x ^ ((i) * 4 & 7)) << 4)]))
 #define GR_FRAGS(st, s, fa, fb)                                                                \
-  _Pragma("unroll") for (int i = 0; i < 4; ++i) fa[i] = GR_FRAG(GR_E(st), a_base, wk, i, s);   \
-  _Pragma("unroll") for (int j = 0; j < 4; ++j) fb[j] = GR_FRAG(GR_D(st), b_base, wn, j, s);
+  _Pragma("unroll") for (int i = 0; i < 4; ++i) fa[i] = GR_FRAG(GR_E(st), a_base, i, s);       \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j) fb[j] = GR_FRAG(GR_D(st), b_base, j, s);
 #define GR_MFMA(fa, fb)                                                                        \
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
 #define GR_FENCE() __builtin_amdgcn_sched_barrier(0)
 #define GR_GROUP(mask, n) __builtin_amdgcn_sched_group_barrier(mask, n, 0)
-// 16 MFMAs, a fragment's read behind each, and between them the conversion of two rows
-#define GR_MIX()                                                                               \
+// 16 MFMAs, between the first of them the next fragments' reads, and V vector instructions
+// and the LDS writes that they lead to, one per W MFMAs
+#define GR_MIX(V, W)                                                                           \
   _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                          \
-    GR_GROUP(0x008, 1); GR_GROUP(0x100, 1); GR_GROUP(0x002, 6);                                \
-    if (g_ % 4 == 3) GR_GROUP(0x200, 1);                                                       \
+    GR_GROUP(0x008, 1);                                                                        \
+    if (g_ < 8) GR_GROUP(0x100, 1);                                                            \
+    GR_GROUP(0x002, V);                                                                        \
+    if (g_ % (W) == (W) - 1) GR_GROUP(0x200, 1);                                               \
   }                                                                                            \
   GR_FENCE();
 #define GR_STEP(kt_, P, Q)                                                                     \
   {                                                                                            \
     GR_FRAGS(P, 1, fa1, fb1)                                                                   \
+    GR_WRITED(Q)                                                                               \
     GR_MFMA(fa0, fb0)                                                                          \
-    _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) { GR_GROUP(0x008, 1); GR_GROUP(0x100, 1); } \
-    GR_FENCE();                                                                                \
+    GR_MIX(2, 2)                                                                               \
+    GR_LOADD((kt_) + 2)                                                                        \
     GR_FRAGS(P, 2, fa0, fb0)                                                                   \
-    GR_WRITE(Q, 0)                                                                             \
-    GR_WRITE(Q, 1)                                                                             \
+    GR_WRITEE(Q, 0)                                                                            \
     GR_MFMA(fa1, fb1)                                                                          \
-    GR_MIX()                                                                                   \
+    GR_MIX(6, 4)                                                                               \
     GR_FRAGS(P, 3, fa1, fb1)                                                                   \
-    GR_WRITE(Q, 2)                                                                             \
-    GR_WRITE(Q, 3)                                                                             \
+    GR_WRITEE(Q, 1)                                                                            \
     GR_MFMA(fa0, fb0)                                                                          \
-    GR_MIX()                                                                                   \
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");                   \
+    GR_MIX(6, 4)                                                                               \
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");                            \
     GR_FENCE();                                                                                \
+    GR_LOADE((kt_) + 2)                                                                        \
     GR_FRAGS(Q, 0, fa0, fb0)                                                                   \
-    GR_LOAD((kt_) + 2, P)                                                                      \
     GR_MFMA(fa1, fb1)                                                                          \
     _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                        \
-      GR_GROUP(0x008, 1); GR_GROUP(0x100, 2); GR_GROUP(0x020, 2);                              \
+      GR_GROUP(0x008, 1); GR_GROUP(0x100, 1); GR_GROUP(0x020, 1);                              \
     }                                                                                          \
     GR_FENCE();                                                                                \
   }
@@ -209,20 +215,20 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
   bf16x8 fa0[4], fb0[4], fa1[4], fb1[4];
   zero_acc(acc);
   if (steps > 0) {
-    GR_LOAD(0, 0)
-    GR_WRITE(0, 0)
-    GR_WRITE(0, 1)
-    GR_WRITE(0, 2)
-    GR_WRITE(0, 3)
-    GR_LOAD(1, 1)
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    GR_LOADD(0)
+    GR_LOADE(0)
+    GR_WRITED(0)
+    GR_LOADD(1)
+    GR_WRITEE(0, 0)
+    GR_WRITEE(0, 1)
+    GR_LOADE(1)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     GR_FENCE();
     GR_FRAGS(0, 0, fa0, fb0)
     for (int kt = 0; kt < steps; kt += 2) {
       GR_STEP(kt, 0, 1)
       GR_STEP(kt + 1, 1, 0)
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
   uint8_t *patch = out + wave * kPatch;
 #pragma unroll
@@ -234,12 +240,19 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
 #undef GR_STEP
 #undef GR_MIX
 #undef GR_GROUP
+#undef GR_CODE
+#undef GR_PAIR
+#undef GR_WORD
+#undef GR_AT
+#undef GR_WRITEE
+#undef GR_WRITED
+#undef GR_LOADE
+#undef GR_LOADD
+#undef GR_ROWS
 #undef GR_FENCE
 #undef GR_MFMA
 #undef GR_FRAGS
 #undef GR_FRAG
-#undef GR_WRITE
-#undef GR_LOAD
 #undef GR_E
 #undef GR_D
 }
