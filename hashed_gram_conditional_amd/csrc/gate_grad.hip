@@ -14,16 +14,16 @@
 // products of h and k, and w = q_w k_w enters it as the product and its rounding error, so
 // that s keeps its relative precision there. Everything else is fp32.
 //
-// A block walks the tokens blockIdx.x, blockIdx.x + gridDim.x, ...; a thread owns 8 columns
-// of every stream and keeps its part of dw in registers over all of them. The blocks' parts
-// are summed by a second launch in a fixed order.
+// Bound by HBM: every byte is read or written once. A block walks the tokens blockIdx.x,
+// blockIdx.x + gridDim.x, ...; a thread owns 8 columns of every stream and keeps its part of
+// dw in registers over all of them. The blocks' parts are summed by a second launch in a
+// fixed order.
 #include "common.h"
 
 namespace {
 
 constexpr int kMaxHc = 8;
 constexpr int kMaxThreads = 1024;
-constexpr int kMaxBlocks = 512;
 
 struct GateGradArgs {
   const int32_t *ids;
@@ -68,8 +68,248 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-// F32: fp32 streams, else bf16. KI8, HI8: keys and value, streams as codes.
+// The sum over a wave, in lane 63, by lane shifts: within rows of 16, then row to row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_shifted(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float sum_to_last(float v) {
+  v = add_shifted<0x111, 0xF>(v);
+  v = add_shifted<0x112, 0xF>(v);
+  v = add_shifted<0x114, 0xF>(v);
+  v = add_shifted<0x118, 0xF>(v);
+  v = add_shifted<0x142, 0xA>(v);
+  return add_shifted<0x143, 0xC>(v);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_shifted(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+__device__ __forceinline__ double sum_to_last(double v) {
+  v = add_shifted<0x111, 0xF>(v);
+  v = add_shifted<0x112, 0xF>(v);
+  v = add_shifted<0x114, 0xF>(v);
+  v = add_shifted<0x118, 0xF>(v);
+  v = add_shifted<0x142, 0xA>(v);
+  return add_shifted<0x143, 0xC>(v);
+}
+
+// What the outputs of one stream take from its sums, which are of the saved numbers
+// without their scales sh, sk, sv: alpha, and with h and k still without theirs
+//   dh = d + ck k w - Bh h,  dk = ch h w - Bk k,  dw = cw h k.
+struct StreamGrad {
+  float alpha, ch, ck, cw, Bh, Bk;
+};
+__device__ __forceinline__ StreamGrad stream_grad(const GateGradArgs &a, float shh, float skk, float sdv,
+                                                  double dot, float sh, float sk, float sv) {
+  const float inv_d = 1.f / (float)a.dim;
+  const float rh = 1.f / sqrtf(shh * sh * sh * inv_d + a.eps);
+  const float rk = 1.f / sqrtf(skk * sk * sk * inv_d + a.eps);
+  const float D = (float)(dot * (double)sh * (double)sk);
+  const float norm = rh * rk / sqrtf((float)a.dim);
+  const float s = D * norm;
+  const float root = sqrtf(fmaxf(fabsf(s), a.clamp));
+  const float z = a.plain ? s : copysignf(root, s);
+  // alpha (1 - alpha) without the difference of two near ones
+  const float small = expf(-fabsf(z));
+  float slope = small / ((1.f + small) * (1.f + small));
+  if (!a.plain) slope = fabsf(s) > a.clamp ? slope / (2.f * root) : 0.f;
+  const float c1 = sdv * sv * slope * norm;
+  StreamGrad g;
+  g.alpha = (z < 0.f ? small : 1.f) / (1.f + small);
+  g.ch = c1 * sh;
+  g.ck = c1 * sk;
+  g.cw = g.ch * sk;
+  g.Bh = D * rh * rh * inv_d * g.ch;
+  g.Bk = D * rk * rk * inv_d * g.ck;
+  return g;
+}
+
+// The outputs of a DEAD position.
+template <bool F32>
+__device__ __forceinline__ void store_dead(const GateGradArgs &a, int64_t t, int cps, int ci) {
+  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m <= a.hc; ++m)
+    engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, zero);
+  if (a.d_h == a.d_out) return;
+  for (int m = 0; m < a.hc; ++m) {
+    engram::Chunk8<F32> d;
+    d.load_nt(a.d_out, (t * a.hc + m) * cps + ci);
+    d.put(a.d_h, (t * a.hc + m) * cps + ci);
+  }
+}
+
+// Up to HC streams, whose numbers of one token a thread holds together: one barrier a
+// token, and the loads of the next token's stream m are issued as soon as this one's are
+// used up, so that a token is in flight while another is worked on. The learned scales lie
+// in LDS as w = q_w k_w rounded to fp32 and what that drops, rounded to bf16. F32: fp32
+// streams, else bf16. KI8, HI8: keys and value, streams as codes.
+constexpr int kTokenThreads = 640;
+
 template <bool F32, bool KI8, bool HI8, int HC>
+__global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGradArgs a) {
+  // products of two bf16 numbers or codes are exact in fp32
+  constexpr bool kExact = !F32 || (KI8 && HI8);
+  extern __shared__ __align__(16) uint8_t w_lds[];
+  __shared__ double red_d[2][kTokenThreads / 64][HC];
+  __shared__ float red[2][kTokenThreads / 64][HC][3];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int nwaves = blockDim.x >> 6;
+  const int cps = a.dim / 8, hc = a.hc;
+  const bool on = tid < cps;
+  const int ci = on ? tid : 0;
+  float *w_hi = reinterpret_cast<float *>(w_lds);
+  uint16_t *w_lo = reinterpret_cast<uint16_t *>(w_lds + (size_t)hc * a.dim * 4);
+  for (int c = tid; c < hc * cps; c += blockDim.x) {
+    engram::Chunk8<true> q, k;
+    q.load(a.q_w, c);
+    k.load(a.k_w, c);
+    float hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      hi[e] = q[e] * k[e];
+      lo[e] = fmaf(q[e], k[e], -hi[e]);
+    }
+    engram::Chunk8<true>::store(w_hi, c, hi);
+    engram::Chunk8<false>::store(w_lo, c, lo);
+  }
+  __syncthreads();
+  float dw[HC][8];
+#pragma unroll
+  for (int m = 0; m < HC; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[m][e] = 0.f;
+  Saved8<HI8, F32> h[HC];
+  Saved8<KI8, F32> k[HC], v;
+  engram::Chunk8<F32> d[HC];
+  int64_t t = blockIdx.x;
+#pragma unroll
+  for (int m = 0; m < HC; ++m) {
+    if (m >= hc) break;
+    h[m].load(a.h, t * hc + m, a.dim, ci);
+    k[m].load(a.kv, t * (hc + 1) + m, a.dim, ci);
+    d[m].load_nt(a.d_out, (t * hc + m) * cps + ci);
+  }
+  v.load(a.kv, t * (hc + 1) + hc, a.dim, ci);
+  int slot = 0;
+  for (; t < a.tokens; t += gridDim.x) {
+    const int64_t next = t + gridDim.x < a.tokens ? t + gridDim.x : t;
+    const bool dead = engram_dead(a.dead_rule, a.ids[t]);
+    if (!dead) {
+      // this lane's stream's scales
+      const int ml = lane < hc ? lane : 0;
+      const float sh = HI8 ? a.h_scales[t * hc + ml] : 1.f;
+      const float sk = KI8 ? a.kv_scales[t * (hc + 1) + ml] : 1.f;
+      const float sv = KI8 ? a.kv_scales[t * (hc + 1) + hc] : 1.f;
+#pragma unroll
+      for (int m = 0; m < HC; ++m) {
+        if (m >= hc) break;
+        float shh = 0.f, skk = 0.f, sdv = 0.f, rest = 0.f;
+        double dot = 0.0;
+        if (on) {
+          engram::Chunk8<true> w;
+          engram::Chunk8<false> lo;
+          w.load(w_hi, m * cps + ci);
+          lo.load(w_lo, m * cps + ci);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float he = h[m][e], ke = k[m][e];
+            shh = fmaf(he, he, shh);
+            skk = fmaf(ke, ke, skk);
+            sdv = fmaf(d[m][e], v[e], sdv);
+            if (kExact) {
+              // p (w + lo) in three parts: the rounded product, its error and p lo
+              const float p = he * ke, x = p * w[e];
+              rest += fmaf(p, w[e], -x);
+              rest = fmaf(p, lo[e], rest);
+              dot += (double)x;
+            } else {
+              dot = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot);
+            }
+          }
+          dot += (double)rest;
+        }
+        shh = sum_to_last(shh);
+        skk = sum_to_last(skk);
+        sdv = sum_to_last(sdv);
+        dot = sum_to_last(dot);
+        if (lane == 63) {
+          red[slot][wave][m][0] = shh;
+          red[slot][wave][m][1] = skk;
+          red[slot][wave][m][2] = sdv;
+          red_d[slot][wave][m] = dot;
+        }
+      }
+      // the next token's barrier stands between these reads and the writes after it
+      __syncthreads();
+      StreamGrad mine;
+      {
+        float shh = 0.f, skk = 0.f, sdv = 0.f;
+        double dot = 0.0;
+        for (int w = 0; w < nwaves; ++w) {
+          shh += red[slot][w][ml][0];
+          skk += red[slot][w][ml][1];
+          sdv += red[slot][w][ml][2];
+          dot += red_d[slot][w][ml];
+        }
+        mine = stream_grad(a, shh, skk, sdv, dot, sh, sk, sv);
+      }
+      slot ^= 1;
+      float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < HC; ++m) {
+        if (m >= hc) break;
+#define ENGRAM_OF_STREAM(x) __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), m))
+        const float alpha = ENGRAM_OF_STREAM(mine.alpha), ch = ENGRAM_OF_STREAM(mine.ch);
+        const float ck = ENGRAM_OF_STREAM(mine.ck), cw = ENGRAM_OF_STREAM(mine.cw);
+        const float Bh = ENGRAM_OF_STREAM(mine.Bh), Bk = ENGRAM_OF_STREAM(mine.Bk);
+#undef ENGRAM_OF_STREAM
+        if (on) {
+          engram::Chunk8<true> w;
+          w.load(w_hi, m * cps + ci);
+          float dh[8], dk[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float he = h[m][e], ke = k[m][e], de = d[m][e];
+            dh[e] = de + (ck * (ke * w[e]) - Bh * he);
+            dk[e] = ch * (he * w[e]) - Bk * ke;
+            dv[e] = fmaf(alpha, de, dv[e]);
+            dw[m][e] = fmaf(cw, he * ke, dw[m][e]);
+          }
+          engram::Chunk8<F32>::store_nt(a.d_h, (t * hc + m) * cps + ci, dh);
+          engram::Chunk8<F32>::store_nt(a.d_kv, (t * (hc + 1) + m) * cps + ci, dk);
+        }
+        h[m].load(a.h, next * hc + m, a.dim, ci);
+        k[m].load(a.kv, next * (hc + 1) + m, a.dim, ci);
+        d[m].load_nt(a.d_out, (next * hc + m) * cps + ci);
+      }
+      if (on) engram::Chunk8<F32>::store_nt(a.d_kv, (t * (hc + 1) + hc) * cps + ci, dv);
+    } else {
+      if (on) store_dead<F32>(a, t, cps, ci);
+#pragma unroll
+      for (int m = 0; m < HC; ++m) {
+        if (m >= hc) break;
+        h[m].load(a.h, next * hc + m, a.dim, ci);
+        k[m].load(a.kv, next * (hc + 1) + m, a.dim, ci);
+        d[m].load_nt(a.d_out, (next * hc + m) * cps + ci);
+      }
+    }
+    v.load(a.kv, next * (hc + 1) + hc, a.dim, ci);
+  }
+  if (a.part != nullptr && on) {
+#pragma unroll
+    for (int m = 0; m < HC; ++m) {
+      if (m >= hc) break;
+      engram::Chunk8<true>::store(a.part, ((int64_t)blockIdx.x * hc + m) * cps + ci, dw[m]);
+    }
+  }
+}
+
+// Any shape, stream by stream: the wider layers and those of more than 4 streams.
+template <bool F32, bool KI8, bool HI8>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) {
   __shared__ double red_d[2][kMaxThreads / 64];
   __shared__ float red[2][kMaxThreads / 64][3];
@@ -78,27 +318,15 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
   const int cps = a.dim / 8;
   const bool on = tid < cps;
   const int ci = on ? tid : 0;
-  const float inv_d = 1.f / (float)a.dim, inv_sqrt_d = 1.f / sqrtf((float)a.dim);
-  float dw[HC][8];
+  float dw[kMaxHc][8];
 #pragma unroll
-  for (int m = 0; m < HC; ++m)
+  for (int m = 0; m < kMaxHc; ++m)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[m][e] = 0.f;
   int slot = 0;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const bool dead = engram_dead(a.dead_rule, a.ids[t]);
-    engram::Chunk8<F32> d;
-    if (dead) {
-      if (on) {
-        const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        for (int m = 0; m <= a.hc; ++m)
-          engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, zero);
-        if (a.d_h != a.d_out)
-          for (int m = 0; m < a.hc; ++m) {
-            d.load_nt(a.d_out, (t * a.hc + m) * cps + ci);
-            d.put(a.d_h, (t * a.hc + m) * cps + ci);
-          }
-      }
+    if (engram_dead(a.dead_rule, a.ids[t])) {
+      if (on) store_dead<F32>(a, t, cps, ci);
       continue;
     }
     Saved8<KI8, F32> v;
@@ -106,10 +334,11 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
     const float sv = KI8 ? a.kv_scales[t * (a.hc + 1) + a.hc] : 1.f;
     float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < HC; ++m) {
+    for (int m = 0; m < kMaxHc; ++m) {
       if (m >= a.hc) break;
       Saved8<HI8, F32> h;
       Saved8<KI8, F32> k;
+      engram::Chunk8<F32> d;
       h.load(a.h, t * a.hc + m, a.dim, ci);
       k.load(a.kv, t * (a.hc + 1) + m, a.dim, ci);
       d.load_nt(a.d_out, (t * a.hc + m) * cps + ci);
@@ -149,29 +378,16 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
         dot += red_d[slot][w];
       }
       slot ^= 1;
-      const float rh = 1.f / sqrtf(shh * sh * sh * inv_d + a.eps);
-      const float rk = 1.f / sqrtf(skk * sk * sk * inv_d + a.eps);
-      const float D = (float)(dot * (double)sh * (double)sk);
-      const float norm = rh * rk * inv_sqrt_d;
-      const float s = D * norm;
-      const float root = sqrtf(fmaxf(fabsf(s), a.clamp));
-      const float z = a.plain ? s : copysignf(root, s);
-      const float small = expf(-fabsf(z));
-      const float alpha = (z < 0.f ? small : 1.f) / (1.f + small);
-      float slope = small / ((1.f + small) * (1.f + small));
-      if (!a.plain) slope = fabsf(s) > a.clamp ? slope / (2.f * root) : 0.f;
-      const float c1 = sdv * sv * slope * norm;
-      const float ch = c1 * sh, ck = c1 * sk;
-      const float Bh = D * rh * rh * inv_d * ch, Bk = D * rk * rk * inv_d * ck;
+      const StreamGrad g = stream_grad(a, shh, skk, sdv, dot, sh, sk, sv);
       if (on) {
         float dh[8], dk[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float w = q[e] * kw[e];
-          dh[e] = d[e] + (ck * (k[e] * w) - Bh * h[e]);
-          dk[e] = ch * (h[e] * w) - Bk * k[e];
-          dv[e] = fmaf(alpha, d[e], dv[e]);
-          dw[m][e] = fmaf(ch * sk, h[e] * k[e], dw[m][e]);
+          dh[e] = d[e] + (g.ck * (k[e] * w) - g.Bh * h[e]);
+          dk[e] = g.ch * (h[e] * w) - g.Bk * k[e];
+          dv[e] = fmaf(g.alpha, d[e], dv[e]);
+          dw[m][e] = fmaf(g.cw, h[e] * k[e], dw[m][e]);
         }
         engram::Chunk8<F32>::store_nt(a.d_h, (t * a.hc + m) * cps + ci, dh);
         engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, dk);
@@ -181,7 +397,7 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
   }
   if (a.part != nullptr && on) {
 #pragma unroll
-    for (int m = 0; m < HC; ++m) {
+    for (int m = 0; m < kMaxHc; ++m) {
       if (m >= a.hc) break;
       engram::Chunk8<true>::store(a.part, ((int64_t)blockIdx.x * a.hc + m) * cps + ci, dw[m]);
     }
@@ -211,20 +427,31 @@ __global__ __launch_bounds__(64 * kSumGroups) void gate_grad_weights_kernel(
   d_k_w[col] = accumulate ? d_k_w[col] + k : k;
 }
 
-int grad_blocks(int64_t tokens) { return (int)(tokens < kMaxBlocks ? tokens : kMaxBlocks); }
+// Blocks of a call: one per CU of the 256, more for narrow layers, whose blocks are small,
+// as far as 16 tokens a block pay for its part of dw.
+int grad_blocks(int64_t tokens, int32_t dim) {
+  const int threads = (dim / 8 + 63) / 64 * 64;
+  const int64_t fit = 256 * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
+  const int64_t paid = tokens / 16 > 256 ? tokens / 16 : 256;
+  const int64_t blocks = fit < paid ? fit : paid;
+  return (int)(tokens < blocks ? tokens : blocks);
+}
 
 template <bool F32, bool KI8, bool HI8>
 void launch(const GateGradArgs &a, int blocks, int threads, hipStream_t stream) {
-  if (a.hc <= 4)
-    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8, 4>), dim3(blocks), dim3(threads), 0, stream, a);
+  const size_t lds = (size_t)a.hc * a.dim * 6;
+  if (a.hc <= 2 && threads <= kTokenThreads)
+    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 2>), dim3(blocks), dim3(threads), lds, stream, a);
+  else if (a.hc <= 4 && threads <= kTokenThreads)
+    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 4>), dim3(blocks), dim3(threads), lds, stream, a);
   else
-    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8, 8>), dim3(blocks), dim3(threads), 0, stream, a);
+    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8>), dim3(blocks), dim3(threads), 0, stream, a);
 }
 
 }  // namespace
 
 size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim) {
-  return (size_t)grad_blocks(tokens) * hc * dim * sizeof(float);
+  return (size_t)grad_blocks(tokens, dim) * hc * dim * sizeof(float);
 }
 
 hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
@@ -248,7 +475,7 @@ hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int3
   a.eps = eps;
   a.clamp = clamp;
   a.plain = plain;
-  const int blocks = grad_blocks(tokens), threads = (dim / 8 + 63) / 64 * 64;
+  const int blocks = grad_blocks(tokens, dim), threads = (dim / 8 + 63) / 64 * 64;
 #define ENGRAM_GATE_GRAD(F)                                                 \
   if (g.kv_i8 && g.h_i8) launch<F, true, true>(a, blocks, threads, stream); \
   else if (g.kv_i8) launch<F, true, false>(a, blocks, threads, stream);     \
