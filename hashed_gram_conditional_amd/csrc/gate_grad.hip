@@ -161,22 +161,6 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
   const int cps = a.dim / 8, hc = a.hc;
   const bool on = tid < cps;
   const int ci = on ? tid : 0;
-  float *w_hi = reinterpret_cast<float *>(w_lds);
-  uint16_t *w_lo = reinterpret_cast<uint16_t *>(w_lds + (size_t)hc * a.dim * 4);
-  for (int c = tid; c < hc * cps; c += blockDim.x) {
-    engram::Chunk8<true> q, k;
-    q.load(a.q_w, c);
-    k.load(a.k_w, c);
-    float hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      hi[e] = q[e] * k[e];
-      lo[e] = fmaf(q[e], k[e], -hi[e]);
-    }
-    engram::Chunk8<true>::store(w_hi, c, hi);
-    engram::Chunk8<false>::store(w_lo, c, lo);
-  }
-  __syncthreads();
   float dw[HC][8];
 #pragma unroll
   for (int m = 0; m < HC; ++m)
@@ -194,6 +178,22 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
     d[m].load_nt(a.d_out, (t * hc + m) * cps + ci);
   }
   v.load(a.kv, t * (hc + 1) + hc, a.dim, ci);
+  float *w_hi = reinterpret_cast<float *>(w_lds);
+  uint16_t *w_lo = reinterpret_cast<uint16_t *>(w_lds + (size_t)hc * a.dim * 4);
+  for (int c = tid; c < hc * cps; c += blockDim.x) {
+    engram::Chunk8<true> q, k;
+    q.load(a.q_w, c);
+    k.load(a.k_w, c);
+    float hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      hi[e] = q[e] * k[e];
+      lo[e] = fmaf(q[e], k[e], -hi[e]);
+    }
+    engram::Chunk8<true>::store(w_hi, c, hi);
+    engram::Chunk8<false>::store(w_lo, c, lo);
+  }
+  __syncthreads();
   int slot = 0;
   for (; t < a.tokens; t += gridDim.x) {
     const int64_t next = t + gridDim.x < a.tokens ? t + gridDim.x : t;

@@ -6,6 +6,7 @@
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kLongThreads = 1024;
 constexpr uint32_t kSmallest = 8u << 23;      // 2^-119
 
 struct RowScale {
@@ -51,43 +52,161 @@ __device__ __forceinline__ float code_of(float x, float inv) {
   return n;
 }
 
-template <bool F32>
-__device__ __forceinline__ float load1(const void *src, int64_t i) {
-  return F32 ? reinterpret_cast<const float *>(src)[i]
-             : engram::bf16_to_f32(reinterpret_cast<const uint16_t *>(src)[i]);
+// Eight consecutive values from `col` on, zeros behind the row. VEC: rows start at multiples
+// of 8 values.
+template <bool F32, bool VEC>
+struct Eight {
+  float f[8];
+  __device__ __forceinline__ void load(const void *src, int64_t row_off, int64_t col, int64_t cols) {
+    if (VEC && col + 8 <= cols) {
+      engram::Chunk8<F32> c;
+      c.load_nt(src, (row_off + col) / 8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = c[e];
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = 0.f;
+      if (col + e < cols)
+        f[e] = F32 ? reinterpret_cast<const float *>(src)[row_off + col + e]
+                   : engram::bf16_to_f32(reinterpret_cast<const uint16_t *>(src)[row_off + col + e]);
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t = max(t, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+    return t;
+  }
+  // the codes, as numbers, in place of the values, and packed
+  template <bool POW2>
+  __device__ __forceinline__ uint2 encode(const RowScale &r) {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // x / s is exact where s is a power of two
+      f[e] = r.bad ? 0.f : POW2 ? rintf(f[e] * r.inv) : code_of(f[e], r.inv);
+      w[e / 4] |= ((uint32_t)(int)f[e] & 0xFFu) << (8 * (e % 4));
+    }
+    return make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ void store(void *dst, int64_t row_off, int64_t col, int64_t cols, float scale) const {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f[e] * scale;
+    if (VEC && col + 8 <= cols) {
+      engram::Chunk8<F32>::store_nt(dst, (row_off + col) / 8, v);
+      // keeps the compiler from merging these with the single stores below
+      asm volatile("" ::: "memory");
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (col + e < cols) {
+        if (F32)
+          reinterpret_cast<float *>(dst)[row_off + col + e] = v[e];
+        else
+          reinterpret_cast<uint16_t *>(dst)[row_off + col + e] = (uint16_t)engram::pack_bf16x2(v[e], v[e]);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, engram::kWave));
+  return v;
 }
 
-template <bool F32, bool POW2>
-__global__ __launch_bounds__(kThreads) void quantize_i8_kernel(const void *src, int64_t cols,
+// A row in the registers of TEAM threads (a wave, or the block), CPT groups of 8 a thread.
+// src and values may be the same buffer (each value is read and written by one thread), so
+// neither is marked restrict.
+template <bool F32, bool VEC, bool POW2, int TEAM, int CPT>
+__global__ __launch_bounds__(kThreads) void quantize_i8_kernel(const void *src, int64_t rows, int64_t cols,
                                                                int64_t ld, int64_t out_cols,
-                                                               int8_t *__restrict__ codes,
-                                                               float *__restrict__ scales,
-                                                               void *values) {
-  __shared__ uint32_t red[kThreads / 64];
-  const int64_t row = blockIdx.x;
+                                                               uint2 *__restrict__ codes,
+                                                               float *__restrict__ scales, void *values) {
+  const int64_t row = TEAM == 64 ? (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6) : blockIdx.x;
+  const int at = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
+  if (TEAM == 64 && row >= rows) return;
+  const int64_t groups = out_cols / 8;
+  Eight<F32, VEC> x[CPT];
   uint32_t top = 0;
-  for (int64_t c = threadIdx.x; c < cols; c += kThreads)
-    top = max(top, __float_as_uint(load1<F32>(src, row * ld + c)) & 0x7FFFFFFFu);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+  for (int i = 0; i < CPT; ++i) x[i].load(src, row * ld, (int64_t)(at + i * TEAM) * 8, cols);
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) top = max(top, x[i].top());
+  top = wave_max(top);
+  if (TEAM != 64) {
+    __shared__ uint32_t red[kThreads / 64];
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) top = max(top, red[w]);
+  }
+  const RowScale r = row_scale<POW2>(top);
+  if (at == 0) scales[row] = r.scale;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int64_t g = at + i * TEAM;
+    if (g >= groups) break;
+    const uint2 w = x[i].template encode<POW2>(r);
+    codes[row * groups + g] = w;
+    if (values != nullptr) x[i].store(values, row * ld, g * 8, cols, r.scale);
+  }
+}
+
+// A longer row: read twice, the second time from L2.
+template <bool F32, bool VEC, bool POW2>
+__global__ __launch_bounds__(kLongThreads) void quantize_i8_long_kernel(const void *src, int64_t cols,
+                                                                        int64_t ld, int64_t out_cols,
+                                                                        uint2 *__restrict__ codes,
+                                                                        float *__restrict__ scales,
+                                                                        void *values) {
+  __shared__ uint32_t red[kLongThreads / 64];
+  const int64_t row = blockIdx.x, groups = out_cols / 8;
+  Eight<F32, VEC> x;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
+    x.load(src, row * ld, g * 8, cols);
+    top = max(top, x.top());
+  }
+  top = wave_max(top);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) top = max(top, red[w]);
+  for (int w = 0; w < kLongThreads / 64; ++w) top = max(top, red[w]);
   const RowScale r = row_scale<POW2>(top);
   if (threadIdx.x == 0) scales[row] = r.scale;
-  for (int64_t c = threadIdx.x; c < out_cols; c += kThreads) {
-    float n = 0.f;
-    if (c < cols && !r.bad) n = code_of(load1<F32>(src, row * ld + c), r.inv);
-    codes[row * out_cols + c] = (int8_t)(int)n;
-    if (values != nullptr && c < cols) {
-      const float v = n * r.scale;
-      if (F32)
-        reinterpret_cast<float *>(values)[row * ld + c] = v;
-      else
-        reinterpret_cast<uint16_t *>(values)[row * ld + c] = (uint16_t)engram::pack_bf16x2(v, v);
-    }
+  for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
+    x.load(src, row * ld, g * 8, cols);
+    const uint2 w = x.template encode<POW2>(r);
+    codes[row * groups + g] = w;
+    if (values != nullptr) x.store(values, row * ld, g * 8, cols, r.scale);
   }
+}
+
+// Rows of up to 1024 columns take a wave each, of up to 8192 a block, in the registers of
+// which they fit; longer ones are read twice.
+template <bool F32, bool VEC, bool POW2>
+void launch(const void *src, int64_t rows, int64_t cols, int64_t ld, int64_t out_cols, uint2 *codes,
+            float *scales, void *values, hipStream_t stream) {
+#define ENGRAM_QUANTIZE(T, C)                                                                   \
+  hipLaunchKernelGGL((quantize_i8_kernel<F32, VEC, POW2, T, C>),                                \
+                     dim3((unsigned)(T == 64 ? (rows + 3) / 4 : rows)), dim3(kThreads), 0, stream, src, \
+                     rows, cols, ld, out_cols, codes, scales, values)
+  if (out_cols <= 512) ENGRAM_QUANTIZE(64, 1);
+  else if (out_cols <= 1024) ENGRAM_QUANTIZE(64, 2);
+  else if (out_cols <= 2048) ENGRAM_QUANTIZE(kThreads, 1);
+  else if (out_cols <= 4096) ENGRAM_QUANTIZE(kThreads, 2);
+  else if (out_cols <= 6144) ENGRAM_QUANTIZE(kThreads, 3);
+  else if (out_cols <= 8192) ENGRAM_QUANTIZE(kThreads, 4);
+  else
+    hipLaunchKernelGGL((quantize_i8_long_kernel<F32, VEC, POW2>), dim3((unsigned)rows), dim3(kLongThreads), 0,
+                       stream, src, cols, ld, out_cols, codes, scales, values);
+#undef ENGRAM_QUANTIZE
 }
 
 }  // namespace
@@ -96,14 +215,21 @@ hipError_t engram_launch_quantize_i8(bool f32, bool pow2, const void *src, int64
                                      int64_t cols, int64_t ld, int64_t out_cols, int8_t *codes,
                                      float *scales, void *values, hipStream_t stream) {
   if (rows <= 0) return hipSuccess;
-  const dim3 grid((unsigned)rows);
-#define ENGRAM_QUANTIZE(F, P)                                                                   \
-  hipLaunchKernelGGL((quantize_i8_kernel<F, P>), grid, dim3(kThreads), 0, stream, src, cols, ld, \
-                     out_cols, codes, scales, values)
-  if (f32 && pow2) ENGRAM_QUANTIZE(true, true);
-  else if (f32) ENGRAM_QUANTIZE(true, false);
-  else if (pow2) ENGRAM_QUANTIZE(false, true);
-  else ENGRAM_QUANTIZE(false, false);
+  uint2 *words = reinterpret_cast<uint2 *>(codes);
+  const bool vec = ld % 8 == 0;
+#define ENGRAM_QUANTIZE(F, V, P) launch<F, V, P>(src, rows, cols, ld, out_cols, words, scales, values, stream)
+#define ENGRAM_QUANTIZE_KIND(F, V) \
+  if (pow2) ENGRAM_QUANTIZE(F, V, true); else ENGRAM_QUANTIZE(F, V, false)
+  if (f32 && vec) {
+    ENGRAM_QUANTIZE_KIND(true, true);
+  } else if (f32) {
+    ENGRAM_QUANTIZE_KIND(true, false);
+  } else if (vec) {
+    ENGRAM_QUANTIZE_KIND(false, true);
+  } else {
+    ENGRAM_QUANTIZE_KIND(false, false);
+  }
+#undef ENGRAM_QUANTIZE_KIND
 #undef ENGRAM_QUANTIZE
   return hipGetLastError();
 }
