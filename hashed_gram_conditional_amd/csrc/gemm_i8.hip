@@ -282,29 +282,31 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
 }
 
 // ---- few blocks: small tiles, the operands streamed far ahead ------------------------
-// A block takes 64 MT tokens against 64 NI weight rows over the whole of K, two waves
-// along each, so that a wave holds 32 MT x 32 NI outputs. Both operands go into a ring of R
-// K-steps. The one barrier of a step stands before its last MFMAs: by then the step's
+// A block of WV waves takes 64 MT tokens against 64 NB weight rows over the whole of K, two
+// waves along the tokens and WV / 2 along the rows, so that a wave holds 32 MT x 32 NI
+// outputs. Both operands go into a ring of R K-steps. The one barrier of a step stands before its last MFMAs: by then the step's
 // slot has been read and takes the loads of step kt + R, and step kt + 1 has landed: of
 // the loads issued, those of the R - 2 steps behind it may be outstanding. Every step
 // issues the same number of loads, and steps are rounded up to a multiple of R with steps
 // of zeros, so the count holds throughout.
-template <int NI, int MT>
+template <int NB, int MT>
 constexpr int ring_of() {
-  return NI * 2 + MT * 2 <= 6 ? 6 : NI + MT <= 4 ? 4 : 3;
+  return NB + MT <= 3 ? 6 : NB + MT <= 4 ? 4 : 3;
 }
 
-template <bool F32, int NI, int MT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <bool F32, int NB, int MT, int WV>
+__global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(WV / 4, WV / 4)))
 void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
-  constexpr int R = ring_of<NI, MT>();
-  constexpr int kRows = 64 * NI, kToks = 64 * MT;
+  constexpr int NI = NB * 4 / WV;
+  constexpr int R = ring_of<NB, MT>();
+  constexpr int kRows = 64 * NB, kToks = 64 * MT;
   constexpr int kSlot = (kRows + kToks) * kStep;        // the W rows, then the e rows
-  constexpr int kLoads = 2 * NI + 2 * MT;               // direct loads of a wave and step
+  constexpr int kLW = kRows / 8 / WV, kLE = kToks / 8 / WV;
+  constexpr int kLoads = kLW + kLE;                     // direct loads of a wave and step
   // one LDS variable per slot: the compiler tells direct loads into up to eight apart
   __shared__ __align__(1024) uint8_t s0[kSlot], s1[kSlot], s2[kSlot];
   __shared__ __align__(1024) uint8_t s3[R > 3 ? kSlot : 16], s4[R > 4 ? kSlot : 16], s5[R > 5 ? kSlot : 16];
-  static_assert(R * kSlot <= 160 * 1024 && 4 * kPatch <= kSlot, "LDS");
+  static_assert(R * kSlot <= 160 * 1024 && WV * kPatch <= kSlot, "LDS");
   // The token tiles of the same rows go to one XCD, eight row tiles at a time.
   const int tiles_m = (int)gridDim.x / tiles_n;
   const int ahead = (int)blockIdx.x / (8 * tiles_m) * 8, left = (int)blockIdx.x - ahead * tiles_m;
@@ -321,10 +323,10 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
   const __amdgpu_buffer_rsrc_t rsE = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<int8_t *>(op.e_codes + (int64_t)m0 * ld), 0, min(kToks, op.M - m0) * ld, kBufferFlags);
   const int dl_c = (lane & 7) ^ (lane >> 3);
-  const int w_v0 = (wave * (kRows / 4) + (lane >> 3)) * ld + dl_c * 16;
-  const int w_v1 = (wave * (kRows / 4) + (lane >> 3)) * ld + (dl_c ^ 1) * 16;
-  const int e_v0 = (wave * (kToks / 4) + (lane >> 3)) * ld + dl_c * 16;
-  const int e_v1 = (wave * (kToks / 4) + (lane >> 3)) * ld + (dl_c ^ 1) * 16;
+  const int w_v0 = (wave * (kRows / WV) + (lane >> 3)) * ld + dl_c * 16;
+  const int w_v1 = (wave * (kRows / WV) + (lane >> 3)) * ld + (dl_c ^ 1) * 16;
+  const int e_v0 = (wave * (kToks / WV) + (lane >> 3)) * ld + dl_c * 16;
+  const int e_v1 = (wave * (kToks / WV) + (lane >> 3)) * ld + (dl_c ^ 1) * 16;
   const int fsw = (frow & 7) ^ ((frow >> 3) & 1);
   const int a_base = (wn * 32 * NI + frow) * kStep, b_base = (kRows + wm * 32 * MT + frow) * kStep;
 #define IK_SLOT(u) ((u) % R == 0 ? s0 : (u) % R == 1 ? s1 : (u) % R == 2 ? s2 : (u) % R == 3 ? s3 : (u) % R == 4 ? s4 : s5)
@@ -332,11 +334,11 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
   {                                                                                            \
     const int left_ = op.K / 16 - (kt_) * 8;                                                   \
     const int wv0_ = dl_c < left_ ? w_v0 : kBehind, wv1_ = (dl_c ^ 1) < left_ ? w_v1 : kBehind; \
-    _Pragma("unroll") for (int i = 0; i < 2 * MT; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
-        rsE, I8_LDS(&IK_SLOT(u)[kRows * kStep + (wave * 2 * MT + i) * 1024]), 16,              \
+    _Pragma("unroll") for (int i = 0; i < kLE; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
+        rsE, I8_LDS(&IK_SLOT(u)[kRows * kStep + (wave * kLE + i) * 1024]), 16,              \
         (i & 1) ? e_v1 : e_v0, i * 8 * ld + (kt_) * kStep, 0, 0);                              \
-    _Pragma("unroll") for (int i = 0; i < 2 * NI; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
-        rsW, I8_LDS(&IK_SLOT(u)[(wave * 2 * NI + i) * 1024]), 16, (i & 1) ? wv1_ : wv0_,       \
+    _Pragma("unroll") for (int i = 0; i < kLW; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
+        rsW, I8_LDS(&IK_SLOT(u)[(wave * kLW + i) * 1024]), 16, (i & 1) ? wv1_ : wv0_,       \
         i * 8 * ld + (kt_) * kStep, 0, 0);                                                     \
   }
 #define IK_FRAGS(u, s, fa, fb)                                                                 \
@@ -349,15 +351,20 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
     acc[i][j] = mfma_i8(fa[i], fb[j], acc[i][j]);
 #define IK_BARRIER()                                                                           \
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((R - 2) * kLoads) : "memory");
+#define IK_MIX()                                                                               \
+  _Pragma("unroll") for (int g_ = 0; g_ < NI + MT; ++g_) { I8_GROUP(0x100, 1); I8_GROUP(0x008, 1); } \
+  I8_FENCE();
 #define IK_STEP(u)                                                                             \
   {                                                                                            \
     IK_FRAGS(u, 1, fa1, fb1)                                                                   \
     IK_MFMA(fa0, fb0)                                                                          \
+    IK_MIX()                                                                                   \
     IK_FRAGS(u, 2, fa0, fb0)                                                                   \
     IK_MFMA(fa1, fb1)                                                                          \
+    IK_MIX()                                                                                   \
     IK_FRAGS(u, 3, fa1, fb1)                                                                   \
     IK_MFMA(fa0, fb0)                                                                          \
-    I8_FENCE();                                                                                \
+    IK_MIX()                                                                                   \
     IK_BARRIER()                                                                               \
     I8_FENCE();                                                                                \
     IK_FRAGS((u) + 1, 0, fa0, fb0)                                                             \
@@ -402,12 +409,13 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
   // every direct load has landed before a slot holds the outputs
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #undef IK_STEP
+#undef IK_MIX
 #undef IK_BARRIER
 #undef IK_MFMA
 #undef IK_FRAGS
 #undef IK_LOAD
   __shared__ __align__(16) float sc[kRows + kToks];
-  for (int x = tid; x < kRows + kToks; x += 256) {
+  for (int x = tid; x < kRows + kToks; x += 64 * WV) {
     const int at = x < kRows ? n0 + x : m0 + x - kRows;
     sc[x] = at < (x < kRows ? op.N : op.M) ? (x < kRows ? op.w_scales : op.e_scales)[at] : 0.f;
   }
@@ -425,10 +433,10 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
 #undef IK_SLOT
 }
 
-template <bool F32, int NI, int MT>
+template <bool F32, int NI, int MT, int WV = 4>
 hipError_t launch_skinny(const I8Operands &op, void *kv, hipStream_t stream) {
   const int tiles_n = (op.N + 64 * NI - 1) / (64 * NI), tiles_m = (op.M + 64 * MT - 1) / (64 * MT);
-  hipLaunchKernelGGL((i8_skinny_kernel<F32, NI, MT>), dim3((unsigned)(tiles_n * tiles_m)), dim3(256), 0,
+  hipLaunchKernelGGL((i8_skinny_kernel<F32, NI, MT, WV>), dim3((unsigned)(tiles_n * tiles_m)), dim3(64 * WV), 0,
                      stream, op, kv, tiles_n);
   return hipGetLastError();
 }
@@ -446,8 +454,8 @@ hipError_t launch_i8(const I8Operands &op, void *kv, hipStream_t stream) {
   };
   if (rounds(64, 64) == 1) return launch_skinny<F32, 1, 1>(op, kv, stream);
   if (rounds(64, 128) == 1) return launch_skinny<F32, 2, 1>(op, kv, stream);
-  if (rounds(128, 128) == 1) return launch_skinny<F32, 2, 2>(op, kv, stream);
-  if (3 * rounds(128, 256) <= 5 * rounds(BM, BN)) return launch_skinny<F32, 4, 2>(op, kv, stream);
+  if (rounds(128, 128) == 1) return launch_skinny<F32, 2, 2, 8>(op, kv, stream);
+  if (3 * rounds(128, 256) <= 5 * rounds(BM, BN)) return launch_skinny<F32, 4, 2, 8>(op, kv, stream);
   const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   hipLaunchKernelGGL((i8_wide_kernel<F32>), dim3((unsigned)(tiles > cus ? cus : tiles)), dim3(kWideThreads),
