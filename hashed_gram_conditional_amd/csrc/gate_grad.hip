@@ -145,22 +145,25 @@ __device__ __forceinline__ void store_dead(const GateGradArgs &a, int64_t t, int
 // Up to HC streams, whose numbers of one token a thread holds together: one barrier a
 // token, and the loads of the next token's stream m are issued as soon as this one's are
 // used up, so that a token is in flight while another is worked on. The learned scales lie
-// in LDS as w = q_w k_w rounded to fp32 and what that drops, rounded to bf16. F32: fp32
-// streams, else bf16. KI8, HI8: keys and value, streams as codes.
+// in LDS as w = q_w k_w rounded to fp32 and what that drops, rounded to bf16. A block has
+// `teams` teams of `width` threads, each on a token of its own, which share w; their parts
+// of dw meet in LDS at the end. F32: fp32 streams, else bf16. KI8, HI8: keys and value,
+// streams as codes.
 constexpr int kTokenThreads = 640;
 
 template <bool F32, bool KI8, bool HI8, int HC>
-__global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGradArgs a) {
+__global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGradArgs a, int width, int teams) {
   // products of two bf16 numbers or codes are exact in fp32
   constexpr bool kExact = !F32 || (KI8 && HI8);
   extern __shared__ __align__(16) uint8_t w_lds[];
   __shared__ double red_d[2][kTokenThreads / 64][HC];
   __shared__ float red[2][kTokenThreads / 64][HC][3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int nwaves = blockDim.x >> 6;
+  const int team = __builtin_amdgcn_readfirstlane(tid / width);
+  const int first_wave = team * (width >> 6), last_wave = first_wave + (width >> 6);
   const int cps = a.dim / 8, hc = a.hc;
-  const bool on = tid < cps;
-  const int ci = on ? tid : 0;
+  const bool on = tid - team * width < cps;
+  const int ci = on ? tid - team * width : 0;
   float dw[HC][8];
 #pragma unroll
   for (int m = 0; m < HC; ++m)
@@ -169,17 +172,21 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
   Saved8<HI8, F32> h[HC];
   Saved8<KI8, F32> k[HC], v;
   engram::Chunk8<F32> d[HC];
-  int64_t t = blockIdx.x;
+  const int64_t stride = (int64_t)gridDim.x * teams;
+  int64_t t = (int64_t)blockIdx.x * teams + team;
+  const int64_t last = a.tokens - 1;
+  const int64_t begin = t < last ? t : last;
 #pragma unroll
   for (int m = 0; m < HC; ++m) {
     if (m >= hc) break;
-    h[m].load(a.h, t * hc + m, a.dim, ci);
-    k[m].load(a.kv, t * (hc + 1) + m, a.dim, ci);
-    d[m].load_nt(a.d_out, (t * hc + m) * cps + ci);
+    h[m].load(a.h, begin * hc + m, a.dim, ci);
+    k[m].load(a.kv, begin * (hc + 1) + m, a.dim, ci);
+    d[m].load_nt(a.d_out, (begin * hc + m) * cps + ci);
   }
-  v.load(a.kv, t * (hc + 1) + hc, a.dim, ci);
+  v.load(a.kv, begin * (hc + 1) + hc, a.dim, ci);
   float *w_hi = reinterpret_cast<float *>(w_lds);
   uint16_t *w_lo = reinterpret_cast<uint16_t *>(w_lds + (size_t)hc * a.dim * 4);
+#pragma unroll 4
   for (int c = tid; c < hc * cps; c += blockDim.x) {
     engram::Chunk8<true> q, k;
     q.load(a.q_w, c);
@@ -195,15 +202,16 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
   }
   __syncthreads();
   int slot = 0;
-  for (; t < a.tokens; t += gridDim.x) {
-    const int64_t next = t + gridDim.x < a.tokens ? t + gridDim.x : t;
-    const bool dead = engram_dead(a.dead_rule, a.ids[t]);
-    if (!dead) {
-      // this lane's stream's scales
-      const int ml = lane < hc ? lane : 0;
-      const float sh = HI8 ? a.h_scales[t * hc + ml] : 1.f;
-      const float sk = KI8 ? a.kv_scales[t * (hc + 1) + ml] : 1.f;
-      const float sv = KI8 ? a.kv_scales[t * (hc + 1) + hc] : 1.f;
+  // every team takes as many turns as the block's first: one barrier a turn
+  for (int64_t turn = (int64_t)blockIdx.x * teams; turn < a.tokens; turn += stride, t += stride) {
+    const bool some = t < a.tokens;
+    const int64_t next = t + stride < a.tokens ? t + stride : last;
+    const bool live = some && !engram_dead(a.dead_rule, a.ids[t]);
+    const int ml = lane < hc ? lane : 0;       // this lane's stream
+    float sh = 1.f, sk = 1.f, sv = 1.f;
+    if (live) {
+      if (HI8) sh = a.h_scales[t * hc + ml];
+      if (KI8) sk = a.kv_scales[t * (hc + 1) + ml], sv = a.kv_scales[t * (hc + 1) + hc];
 #pragma unroll
       for (int m = 0; m < HC; ++m) {
         if (m >= hc) break;
@@ -243,13 +251,15 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
           red_d[slot][wave][m] = dot;
         }
       }
-      // the next token's barrier stands between these reads and the writes after it
-      __syncthreads();
+    }
+    // the next turn's barrier stands between the reads behind this one and the writes after it
+    __syncthreads();
+    if (live) {
       StreamGrad mine;
       {
         float shh = 0.f, skk = 0.f, sdv = 0.f;
         double dot = 0.0;
-        for (int w = 0; w < nwaves; ++w) {
+        for (int w = first_wave; w < last_wave; ++w) {
           shh += red[slot][w][ml][0];
           skk += red[slot][w][ml][1];
           sdv += red[slot][w][ml][2];
@@ -257,7 +267,6 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
         }
         mine = stream_grad(a, shh, skk, sdv, dot, sh, sk, sv);
       }
-      slot ^= 1;
       float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int m = 0; m < HC; ++m) {
@@ -288,7 +297,7 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
       }
       if (on) engram::Chunk8<F32>::store_nt(a.d_kv, (t * (hc + 1) + hc) * cps + ci, dv);
     } else {
-      if (on) store_dead<F32>(a, t, cps, ci);
+      if (some && on) store_dead<F32>(a, t, cps, ci);
 #pragma unroll
       for (int m = 0; m < HC; ++m) {
         if (m >= hc) break;
@@ -298,8 +307,32 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
       }
     }
     v.load(a.kv, next * (hc + 1) + hc, a.dim, ci);
+    slot ^= 1;
   }
-  if (a.part != nullptr && on) {
+  if (a.part == nullptr) return;
+  // team 0 adds the others' parts, one after another, in w's place
+  for (int other = 1; other < teams; ++other) {
+    __syncthreads();
+    if (team == other && on) {
+#pragma unroll
+      for (int m = 0; m < HC; ++m) {
+        if (m >= hc) break;
+        engram::Chunk8<true>::store(w_hi, m * cps + ci, dw[m]);
+      }
+    }
+    __syncthreads();
+    if (team == 0 && on) {
+#pragma unroll
+      for (int m = 0; m < HC; ++m) {
+        if (m >= hc) break;
+        engram::Chunk8<true> o;
+        o.load(w_hi, m * cps + ci);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[m][e] += o[e];
+      }
+    }
+  }
+  if (team == 0 && on) {
 #pragma unroll
     for (int m = 0; m < HC; ++m) {
       if (m >= hc) break;
@@ -436,31 +469,39 @@ __global__ __launch_bounds__(64 * kSumGroups) void gate_grad_weights_kernel(
   d_k_w[col] = accumulate ? d_k_w[col] + k : k;
 }
 
-// Blocks of a call: one per CU of the 256, more for narrow layers, whose blocks are small,
-// as far as 4 tokens a block pay for its part of dw.
-int grad_blocks(int64_t tokens, int32_t dim) {
-  const int threads = (dim / 8 + 63) / 64 * 64;
-  const int64_t fit = 256 * (threads > 512 ? 1 : threads > 256 ? 2 : 4);
-  const int64_t paid = tokens / 4 > 256 ? tokens / 4 : 256;
-  const int64_t blocks = fit < paid ? fit : paid;
-  return (int)(tokens < blocks ? tokens : blocks);
+// The launch of a shape: threads a token, teams a block, blocks. The token kernel takes one
+// block of wide rows (up to 640 threads) a CU, of the 256, or two of narrow ones, whose
+// teams fill 512 threads.
+struct GateGradPlan {
+  bool by_token;
+  int width, teams, blocks;
+};
+GateGradPlan plan_of(int64_t tokens, int32_t hc, int32_t dim) {
+  GateGradPlan p;
+  p.width = (dim / 8 + 63) / 64 * 64;
+  p.by_token = hc <= 4 && p.width <= kTokenThreads;
+  p.teams = p.by_token && p.width <= 256 ? 512 / p.width : 1;
+  const int64_t most = p.teams > 1 ? 512 : 256, turns = (tokens + p.teams - 1) / p.teams;
+  p.blocks = (int)(turns < most ? turns : most);
+  return p;
 }
 
 template <bool F32, bool KI8, bool HI8>
-void launch(const GateGradArgs &a, int blocks, int threads, hipStream_t stream) {
+void launch(const GateGradArgs &a, const GateGradPlan &p, hipStream_t stream) {
+  const dim3 grid(p.blocks), block(p.width * p.teams);
   const size_t lds = (size_t)a.hc * a.dim * 6;
-  if (a.hc <= 2 && threads <= kTokenThreads)
-    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 2>), dim3(blocks), dim3(threads), lds, stream, a);
-  else if (a.hc <= 4 && threads <= kTokenThreads)
-    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 4>), dim3(blocks), dim3(threads), lds, stream, a);
+  if (!p.by_token)
+    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8>), grid, block, 0, stream, a);
+  else if (a.hc <= 2)
+    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 2>), grid, block, lds, stream, a, p.width, p.teams);
   else
-    hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8>), dim3(blocks), dim3(threads), 0, stream, a);
+    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 4>), grid, block, lds, stream, a, p.width, p.teams);
 }
 
 }  // namespace
 
 size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim) {
-  return (size_t)grad_blocks(tokens, dim) * hc * dim * sizeof(float);
+  return (size_t)plan_of(tokens, hc, dim).blocks * hc * dim * sizeof(float);
 }
 
 hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
@@ -484,12 +525,12 @@ hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int3
   a.eps = eps;
   a.clamp = clamp;
   a.plain = plain;
-  const int blocks = grad_blocks(tokens, dim), threads = (dim / 8 + 63) / 64 * 64;
+  const GateGradPlan p = plan_of(tokens, hc, dim);
 #define ENGRAM_GATE_GRAD(F)                                                 \
-  if (g.kv_i8 && g.h_i8) launch<F, true, true>(a, blocks, threads, stream); \
-  else if (g.kv_i8) launch<F, true, false>(a, blocks, threads, stream);     \
-  else if (g.h_i8) launch<F, false, true>(a, blocks, threads, stream);      \
-  else launch<F, false, false>(a, blocks, threads, stream)
+  if (g.kv_i8 && g.h_i8) launch<F, true, true>(a, p, stream); \
+  else if (g.kv_i8) launch<F, true, false>(a, p, stream);     \
+  else if (g.h_i8) launch<F, false, true>(a, p, stream);      \
+  else launch<F, false, false>(a, p, stream)
   if (tokens <= 0) {
     a.part = g.d_q_w;      // no part is read
   } else if (g.f32) {
@@ -502,6 +543,6 @@ hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int3
   if (err != hipSuccess || a.part == nullptr) return err;
   const int n = hc * dim;
   hipLaunchKernelGGL(gate_grad_weights_kernel, dim3((n + 63) / 64), dim3(64 * kSumGroups), 0, stream,
-                     g.workspace, blocks, n, g.q_w, g.k_w, g.d_q_w, g.d_k_w, g.accumulate);
+                     g.workspace, p.blocks, n, g.q_w, g.k_w, g.d_q_w, g.d_k_w, g.accumulate);
   return hipGetLastError();
 }

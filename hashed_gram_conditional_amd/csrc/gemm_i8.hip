@@ -90,14 +90,6 @@ __device__ __forceinline__ void store_patch(const i32x16 &a0, const i32x16 &a1, 
 // are in flight while the finished tile is stored, and the stores while the next begins.
 // An odd number of steps is rounded up with a step of zeros, so that a tile begins in
 // stage 0.
-//
-// The 32 blocks of an XCD work on 8 x 4 tiles, so that 12 panels of 256 rows serve 32 x 2.
-// Where all of them ask for a line that L2 does not hold, they all wait for memory. So each
-// block asks for its share of the lines two steps ahead of their loads, one 4-byte load a
-// line into LDS that nobody reads. (32768 x 25600 from 6144 inputs 4.53 -> 4.40 ms; with
-// codes of zero 4.07 -> 3.50, so that the rest is the clock under power: 2.3 POPS at 1.8 GHz
-// and 59 % of the matrix units' cycles, where an MFMA loop of nothing else reaches 3.3 on
-// such codes and 4.3 on zeros.) Which lines a block takes matters for speed alone.
 template <bool F32>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles_n) {
@@ -106,7 +98,6 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
   __shared__ __align__(1024) uint8_t w0[BN * kStep], w1[BN * kStep];
   __shared__ __align__(1024) uint8_t e0[BM * kStep], e1[BM * kStep];
   __shared__ __align__(1024) uint8_t out[4 * kPatch];
-  __shared__ __align__(1024) uint8_t unread[4 * 256];
   __shared__ __align__(16) float sc[2][BN + BM];          // the tile's scales, by its parity
   const int tiles = tiles_m * tiles_n;
   const int ke = ((op.K + kStep - 1) / kStep + 1) & ~1;
@@ -122,11 +113,6 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
   const int frow = lane & 31, h = lane >> 5;
   const int fsw = (frow & 7) ^ ((frow >> 3) & 1);
   const int a_base = (wn * 128 + frow) * kStep, b_base = (wm * 128 + frow) * kStep;
-  // the rows whose lines this lane asks for early: 64 of e's shared by 4 blocks (waves 0
-  // and 1), 32 of W's shared by 8 (waves 2 and 3)
-  const int place = (int)blockIdx.x / kXcds % 32;
-  const int early = lane >= (wave < 2 ? 32 : 16) ? kBehind
-                    : ld * (wave < 2 ? place / 8 * 64 + wave * 32 + lane : place % 8 * 32 + wave % 2 * 16 + lane);
   __amdgpu_buffer_rsrc_t rsW, rsE, rsS;
 // The operands of tile t_, from which the loads come; behind the last tile nothing does.
 // Waves 0 and 1 load W's scales, 2 and 3 e's.
@@ -170,14 +156,9 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
 #define I8_MFMA(fa, fb)                                                                        \
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = mfma_i8(fa[i], fb[j], acc[i][j]);
-#define I8_EARLY(kt_)                                                                          \
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(wave < 2 ? rsE : rsW, I8_LDS(unread + wave * 256), 4, \
-                                           (kt_) < ke ? early : kBehind, (kt_) * kStep, 0, 0);
-// the last load issued is an early one
-#define I8_BARRIER() asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#define I8_BARRIER() asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 // the first step of a tile: the stores of the one before may be outstanding, all of them
-// (as many as the counter holds), as they were issued behind the loads; the early load
-// stands before them
+// (as many as the counter holds), as they were issued behind the loads
 #define I8_BARRIER0()                                                                          \
   if (stores)                                                                                  \
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(F32 ? 63 : 32) : "memory"); \
@@ -203,8 +184,6 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
     I8_FRAGS(Q, 0, fa0, fb0)                                                                   \
     I8_LOADSTEP(ahead, P)                                                                      \
     LOAD                                                                                       \
-    I8_FENCE();                                                                                \
-    I8_EARLY((ahead) + 2)                                                                      \
     I8_MFMA(fa1, fb1)                                                                          \
     _Pragma("unroll") for (int g_ = 0; g_ < 16; ++g_) {                                        \
       I8_GROUP(0x008, 1); I8_GROUP(0x100, 2); I8_GROUP(0x020, 2);                              \
@@ -221,7 +200,7 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
   I8_LOADS(0)
   I8_LOADSTEP(0, 0)
   I8_LOADSTEP(1, 1)
-  asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+  I8_BARRIER()
   bool stores = false;                // a whole tile's stores were issued behind the loads
   int par = 0;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -269,7 +248,6 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
 #undef I8_ZERO
 #undef I8_STEP
 #undef I8_PART
-#undef I8_EARLY
 #undef I8_BARRIER0
 #undef I8_BARRIER
 #undef I8_MFMA
