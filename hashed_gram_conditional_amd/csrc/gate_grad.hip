@@ -47,6 +47,12 @@ struct Saved8 {
     c.load_nt(p, row * (dim / 8) + ci);
   }
   __device__ __forceinline__ float operator[](int e) const { return c[e]; }
+  __device__ __forceinline__ float squares() const {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(c[e], c[e], s);
+    return s;
+  }
 };
 template <bool F32>
 struct Saved8<true, F32> {
@@ -60,6 +66,10 @@ struct Saved8<true, F32> {
   __device__ __forceinline__ float operator[](int e) const {
     return (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
   }
+  __device__ __forceinline__ float squares() const {
+    return (float)__builtin_amdgcn_sdot4((int)w[1], (int)w[1],
+                                         __builtin_amdgcn_sdot4((int)w[0], (int)w[0], 0, false), false);
+  }
 };
 
 __device__ __forceinline__ double warp_sum_d(double v) {
@@ -68,33 +78,51 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
-// The sum over a wave, in lane 63, by lane shifts: within rows of 16, then row to row.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float add_shifted(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+// Sums of HC (2 or 4) numbers over a wave: first halves of the wave change places between two
+// streams' numbers, then rows of 16, so that each addition serves two streams; then a row's
+// (half's) lanes by shifts. Stream m's sum ends in lane 64 / HC (m + 1) - 1.
+template <typename T, int CTRL, int ROWS>
+__device__ __forceinline__ T shifted(T v) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, true));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  }
 }
-__device__ __forceinline__ float sum_to_last(float v) {
-  v = add_shifted<0x111, 0xF>(v);
-  v = add_shifted<0x112, 0xF>(v);
-  v = add_shifted<0x114, 0xF>(v);
-  v = add_shifted<0x118, 0xF>(v);
-  v = add_shifted<0x142, 0xA>(v);
-  return add_shifted<0x143, 0xC>(v);
+// a's sums of lanes l and l + 32 (l and l + 16 of each half) below b's
+template <typename T, bool HALVES>
+__device__ __forceinline__ T fold(T a, T b) {
+  constexpr int kWords = sizeof(T) / 4;
+  uint32_t x[kWords], y[kWords];
+  __builtin_memcpy(x, &a, sizeof(T));
+  __builtin_memcpy(y, &b, sizeof(T));
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const auto r = HALVES ? __builtin_amdgcn_permlane32_swap(x[w], y[w], false, false)
+                          : __builtin_amdgcn_permlane16_swap(x[w], y[w], false, false);
+    x[w] = r[0];
+    y[w] = r[1];
+  }
+  __builtin_memcpy(&a, x, sizeof(T));
+  __builtin_memcpy(&b, y, sizeof(T));
+  return a + b;
 }
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double add_shifted(double v) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
-  return v + __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
-}
-__device__ __forceinline__ double sum_to_last(double v) {
-  v = add_shifted<0x111, 0xF>(v);
-  v = add_shifted<0x112, 0xF>(v);
-  v = add_shifted<0x114, 0xF>(v);
-  v = add_shifted<0x118, 0xF>(v);
-  v = add_shifted<0x142, 0xA>(v);
-  return add_shifted<0x143, 0xC>(v);
+template <typename T, int HC>
+__device__ __forceinline__ T sums_of(const T (&v)[HC]) {
+  T s;
+  if constexpr (HC == 4)
+    s = fold<T, false>(fold<T, true>(v[0], v[2]), fold<T, true>(v[1], v[3]));
+  else
+    s = fold<T, true>(v[0], v[1]);
+  s += shifted<T, 0x111, 0xF>(s);
+  s += shifted<T, 0x112, 0xF>(s);
+  s += shifted<T, 0x114, 0xF>(s);
+  s += shifted<T, 0x118, 0xF>(s);
+  if constexpr (HC == 2) s += shifted<T, 0x142, 0xA>(s);     // a row's last lane to the next row
+  return s;
 }
 
 // What the outputs of one stream take from its sums, which are of the saved numbers
@@ -212,44 +240,45 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
     if (live) {
       if (HI8) sh = a.h_scales[t * hc + ml];
       if (KI8) sk = a.kv_scales[t * (hc + 1) + ml], sv = a.kv_scales[t * (hc + 1) + hc];
+float shh[HC], skk[HC], sdv[HC];
+      double dot[HC];
 #pragma unroll
       for (int m = 0; m < HC; ++m) {
-        if (m >= hc) break;
-        float shh = 0.f, skk = 0.f, sdv = 0.f, rest = 0.f;
-        double dot = 0.0;
-        if (on) {
+        shh[m] = skk[m] = sdv[m] = 0.f;
+        dot[m] = 0.0;
+        if (m < hc && on) {
+          float rest = 0.f;
           engram::Chunk8<true> w;
           engram::Chunk8<false> lo;
           w.load(w_hi, m * cps + ci);
           lo.load(w_lo, m * cps + ci);
+          shh[m] = h[m].squares();
+          skk[m] = k[m].squares();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float he = h[m][e], ke = k[m][e];
-            shh = fmaf(he, he, shh);
-            skk = fmaf(ke, ke, skk);
-            sdv = fmaf(d[m][e], v[e], sdv);
+            sdv[m] = fmaf(d[m][e], v[e], sdv[m]);
             if (kExact) {
               // p (w + lo) in three parts: the rounded product, its error and p lo
               const float p = he * ke, x = p * w[e];
               rest += fmaf(p, w[e], -x);
               rest = fmaf(p, lo[e], rest);
-              dot += (double)x;
+              dot[m] += (double)x;
             } else {
-              dot = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot);
+              dot[m] = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot[m]);
             }
           }
-          dot += (double)rest;
+          dot[m] += (double)rest;
         }
-        shh = sum_to_last(shh);
-        skk = sum_to_last(skk);
-        sdv = sum_to_last(sdv);
-        dot = sum_to_last(dot);
-        if (lane == 63) {
-          red[slot][wave][m][0] = shh;
-          red[slot][wave][m][1] = skk;
-          red[slot][wave][m][2] = sdv;
-          red_d[slot][wave][m] = dot;
-        }
+      }
+      const float a0 = sums_of(shh), a1 = sums_of(skk), a2 = sums_of(sdv);
+      const double a3 = sums_of(dot);
+      if (lane % (64 / HC) == 64 / HC - 1) {
+        const int m = lane / (64 / HC);
+        red[slot][wave][m][0] = a0;
+        red[slot][wave][m][1] = a1;
+        red[slot][wave][m][2] = a2;
+        red_d[slot][wave][m] = a3;
       }
     }
     // the next turn's barrier stands between the reads behind this one and the writes after it
