@@ -36,6 +36,7 @@ SCALE_F32 = 0
 SCALE_POW2 = 1
 MAX_I8_IN_DIM = 131056
 MAX_GRAD_OUT_DIM = 1 << 23
+MAX_GRAD_TOKENS = 1 << 30
 MAX_EMBED_DIM = 32768
 MAX_EMBED_GRAD_IDS = 1 << 28
 

@@ -338,10 +338,11 @@ bool i8_product_shape_ok(int64_t tokens, int64_t in_dim, int64_t out_dim) {
   return bf16_projection_shape_ok(tokens, in_dim, out_dim);
 }
 
-// The weight's gradient also addresses 64 rows of d_kv through 32-bit byte counts and numbers
-// its 256 x 256 tiles (times their splits) and groups of 4 gradients in 32-bit grids.
+// The weight's gradient also addresses 64 rows of d_kv through 32-bit byte counts, and counts
+// tokens beyond the last in 32 bits.
 bool i8_gradient_shape_ok(int64_t tokens, int64_t in_dim, int64_t out_dim) {
-  return i8_product_shape_ok(tokens, in_dim, out_dim) && out_dim <= ENGRAM_MAX_GRAD_OUT_DIM;
+  return i8_product_shape_ok(tokens, in_dim, out_dim) && out_dim <= ENGRAM_MAX_GRAD_OUT_DIM &&
+         tokens <= ENGRAM_MAX_GRAD_TOKENS;
 }
 
 // The last HIP error an entry point returned ENGRAM_EHIP for, per host thread.
@@ -1324,7 +1325,8 @@ int engram_project_i8(const void *e_codes, const float *e_scales, const void *w_
 
 size_t engram_gate_grad_workspace_size(const engram_forward_desc *desc) {
   if (check_desc(desc) != ENGRAM_OK) return 0;
-  return engram_gate_grad_workspace(desc->batch * desc->seq, desc->hc, desc->dim);
+  return engram_gate_grad_workspace(desc->row_format == ENGRAM_ROW_F32, desc->batch * desc->seq,
+                                    desc->hc, desc->dim);
 }
 
 int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_t raw_vocab,
@@ -1357,7 +1359,7 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
       return ENGRAM_EINVAL;
     if (d_q_w != nullptr &&
         (workspace == nullptr || !aligned(workspace, 256) ||
-         workspace_bytes < engram_gate_grad_workspace(ntok, desc->hc, desc->dim)))
+         workspace_bytes < engram_gate_grad_workspace_size(desc)))
       return ENGRAM_EWORKSPACE;
   }
   EngramGateGrad g;

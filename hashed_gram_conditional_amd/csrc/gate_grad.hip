@@ -22,7 +22,6 @@
 
 namespace {
 
-constexpr int kMaxHc = 8;
 constexpr int kMaxThreads = 1024;
 
 struct GateGradArgs {
@@ -177,15 +176,18 @@ __device__ __forceinline__ void store_dead(const GateGradArgs &a, int64_t t, int
 // `teams` teams of `width` threads, each on a token of its own, which share w; their parts
 // of dw meet in LDS at the end. F32: fp32 streams, else bf16. KI8, HI8: keys and value,
 // streams as codes.
-constexpr int kTokenThreads = 640;
+constexpr int token_threads(bool f32, int hc) { return f32 || hc > 4 ? 512 : 640; }
+constexpr int kMaxTokenThreads = 640;
+constexpr int kTokenColumns = 25600;          // hc * dim: 150 KB of w
 
 template <bool F32, bool KI8, bool HI8, int HC>
-__global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGradArgs a, int width, int teams) {
+__global__ __launch_bounds__(token_threads(F32, HC)) void gate_grad_token_kernel(GateGradArgs a, int width, int teams) {
   // products of two bf16 numbers or codes are exact in fp32
   constexpr bool kExact = !F32 || (KI8 && HI8);
+  constexpr int kFold = HC < 4 ? HC : 4;      // streams whose sums are formed together
   extern __shared__ __align__(16) uint8_t w_lds[];
-  __shared__ double red_d[2][kTokenThreads / 64][HC];
-  __shared__ float red[2][kTokenThreads / 64][HC][3];
+  __shared__ double red_d[2][kMaxTokenThreads / 64][HC];
+  __shared__ float red[2][kMaxTokenThreads / 64][HC][3];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int team = __builtin_amdgcn_readfirstlane(tid / width);
   const int first_wave = team * (width >> 6), last_wave = first_wave + (width >> 6);
@@ -240,45 +242,49 @@ __global__ __launch_bounds__(kTokenThreads) void gate_grad_token_kernel(GateGrad
     if (live) {
       if (HI8) sh = a.h_scales[t * hc + ml];
       if (KI8) sk = a.kv_scales[t * (hc + 1) + ml], sv = a.kv_scales[t * (hc + 1) + hc];
-float shh[HC], skk[HC], sdv[HC];
-      double dot[HC];
 #pragma unroll
-      for (int m = 0; m < HC; ++m) {
-        shh[m] = skk[m] = sdv[m] = 0.f;
-        dot[m] = 0.0;
-        if (m < hc && on) {
-          float rest = 0.f;
-          engram::Chunk8<true> w;
-          engram::Chunk8<false> lo;
-          w.load(w_hi, m * cps + ci);
-          lo.load(w_lo, m * cps + ci);
-          shh[m] = h[m].squares();
-          skk[m] = k[m].squares();
+      for (int g = 0; g < HC; g += kFold) {
+        float shh[kFold], skk[kFold], sdv[kFold];
+        double dot[kFold];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float he = h[m][e], ke = k[m][e];
-            sdv[m] = fmaf(d[m][e], v[e], sdv[m]);
-            if (kExact) {
-              // p (w + lo) in three parts: the rounded product, its error and p lo
-              const float p = he * ke, x = p * w[e];
-              rest += fmaf(p, w[e], -x);
-              rest = fmaf(p, lo[e], rest);
-              dot[m] += (double)x;
-            } else {
-              dot[m] = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot[m]);
+        for (int x = 0; x < kFold; ++x) {
+          const int m = g + x;
+          shh[x] = skk[x] = sdv[x] = 0.f;
+          dot[x] = 0.0;
+          if (m < hc && on) {
+            float rest = 0.f;
+            engram::Chunk8<true> w;
+            engram::Chunk8<false> lo;
+            w.load(w_hi, m * cps + ci);
+            lo.load(w_lo, m * cps + ci);
+            shh[x] = h[m].squares();
+            skk[x] = k[m].squares();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float he = h[m][e], ke = k[m][e];
+              sdv[x] = fmaf(d[m][e], v[e], sdv[x]);
+              if (kExact) {
+                // p (w + lo) in three parts: the rounded product, its error and p lo
+                const float p = he * ke, r = p * w[e];
+                rest += fmaf(p, w[e], -r);
+                rest = fmaf(p, lo[e], rest);
+                dot[x] += (double)r;
+              } else {
+                dot[x] = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot[x]);
+              }
             }
+            dot[x] += (double)rest;
           }
-          dot[m] += (double)rest;
         }
-      }
-      const float a0 = sums_of(shh), a1 = sums_of(skk), a2 = sums_of(sdv);
-      const double a3 = sums_of(dot);
-      if (lane % (64 / HC) == 64 / HC - 1) {
-        const int m = lane / (64 / HC);
-        red[slot][wave][m][0] = a0;
-        red[slot][wave][m][1] = a1;
-        red[slot][wave][m][2] = a2;
-        red_d[slot][wave][m] = a3;
+        const float a0 = sums_of(shh), a1 = sums_of(skk), a2 = sums_of(sdv);
+        const double a3 = sums_of(dot);
+        if (lane % (64 / kFold) == 64 / kFold - 1) {
+          const int m = g + lane / (64 / kFold);
+          red[slot][wave][m][0] = a0;
+          red[slot][wave][m][1] = a1;
+          red[slot][wave][m][2] = a2;
+          red_d[slot][wave][m] = a3;
+        }
       }
     }
     // the next turn's barrier stands between the reads behind this one and the writes after it
@@ -370,7 +376,8 @@ float shh[HC], skk[HC], sdv[HC];
   }
 }
 
-// Any shape, stream by stream: the wider layers and those of more than 4 streams.
+// Any shape, stream by stream, for layers too wide for the other; the block's part of dw is
+// added up in the workspace, each value by one thread.
 template <bool F32, bool KI8, bool HI8>
 __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) {
   __shared__ double red_d[2][kMaxThreads / 64];
@@ -380,11 +387,11 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
   const int cps = a.dim / 8;
   const bool on = tid < cps;
   const int ci = on ? tid : 0;
-  float dw[kMaxHc][8];
-#pragma unroll
-  for (int m = 0; m < kMaxHc; ++m)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[m][e] = 0.f;
+  float *part = a.part == nullptr ? nullptr : a.part + (int64_t)blockIdx.x * a.hc * a.dim;
+  if (part != nullptr && on) {
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < a.hc; ++m) engram::Chunk8<true>::store(part, m * cps + ci, zero);
+  }
   int slot = 0;
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     if (engram_dead(a.dead_rule, a.ids[t])) {
@@ -395,9 +402,7 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
     v.load(a.kv, t * (a.hc + 1) + a.hc, a.dim, ci);
     const float sv = KI8 ? a.kv_scales[t * (a.hc + 1) + a.hc] : 1.f;
     float dv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int m = 0; m < kMaxHc; ++m) {
-      if (m >= a.hc) break;
+    for (int m = 0; m < a.hc; ++m) {
       Saved8<HI8, F32> h;
       Saved8<KI8, F32> k;
       engram::Chunk8<F32> d;
@@ -449,20 +454,20 @@ __global__ __launch_bounds__(kMaxThreads) void gate_grad_kernel(GateGradArgs a) 
           dh[e] = d[e] + (g.ck * (k[e] * w) - g.Bh * h[e]);
           dk[e] = g.ch * (h[e] * w) - g.Bk * k[e];
           dv[e] = fmaf(g.alpha, d[e], dv[e]);
-          dw[m][e] = fmaf(g.cw, h[e] * k[e], dw[m][e]);
+        }
+        if (part != nullptr) {
+          engram::Chunk8<true> sum;
+          sum.load(part, m * cps + ci);
+          float dw[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dw[e] = fmaf(g.cw, h[e] * k[e], sum[e]);
+          engram::Chunk8<true>::store(part, m * cps + ci, dw);
         }
         engram::Chunk8<F32>::store_nt(a.d_h, (t * a.hc + m) * cps + ci, dh);
         engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + m) * cps + ci, dk);
       }
     }
     if (on) engram::Chunk8<F32>::store_nt(a.d_kv, (t * (a.hc + 1) + a.hc) * cps + ci, dv);
-  }
-  if (a.part != nullptr && on) {
-#pragma unroll
-    for (int m = 0; m < kMaxHc; ++m) {
-      if (m >= a.hc) break;
-      engram::Chunk8<true>::store(a.part, ((int64_t)blockIdx.x * a.hc + m) * cps + ci, dw[m]);
-    }
   }
 }
 
@@ -499,18 +504,20 @@ __global__ __launch_bounds__(64 * kSumGroups) void gate_grad_weights_kernel(
 }
 
 // The launch of a shape: threads a token, teams a block, blocks. The token kernel takes one
-// block of wide rows (up to 640 threads) a CU, of the 256, or two of narrow ones, whose
-// teams fill 512 threads.
+// block of wide rows a CU, of the 256, or two of narrow ones, whose teams fill 512 threads;
+// the other up to four, as their threads allow.
 struct GateGradPlan {
   bool by_token;
   int width, teams, blocks;
 };
-GateGradPlan plan_of(int64_t tokens, int32_t hc, int32_t dim) {
+GateGradPlan plan_of(bool f32, int64_t tokens, int32_t hc, int32_t dim) {
   GateGradPlan p;
   p.width = (dim / 8 + 63) / 64 * 64;
-  p.by_token = hc <= 4 && p.width <= kTokenThreads;
+  // eight streams of fp32 numbers do not fit the registers
+  p.by_token = p.width <= token_threads(f32, hc) && hc * dim <= kTokenColumns && (!f32 || hc <= 4);
   p.teams = p.by_token && p.width <= 256 ? 512 / p.width : 1;
-  const int64_t most = p.teams > 1 ? 512 : 256, turns = (tokens + p.teams - 1) / p.teams;
+  const int64_t most = p.by_token ? (p.teams > 1 ? 512 : 256) : p.width <= 128 ? 1024 : p.width <= 320 ? 512 : 256;
+  const int64_t turns = (tokens + p.teams - 1) / p.teams;
   p.blocks = (int)(turns < most ? turns : most);
   return p;
 }
@@ -523,14 +530,16 @@ void launch(const GateGradArgs &a, const GateGradPlan &p, hipStream_t stream) {
     hipLaunchKernelGGL((gate_grad_kernel<F32, KI8, HI8>), grid, block, 0, stream, a);
   else if (a.hc <= 2)
     hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 2>), grid, block, lds, stream, a, p.width, p.teams);
-  else
+  else if (a.hc <= 4)
     hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 4>), grid, block, lds, stream, a, p.width, p.teams);
+  else if constexpr (!F32)
+    hipLaunchKernelGGL((gate_grad_token_kernel<F32, KI8, HI8, 8>), grid, block, lds, stream, a, p.width, p.teams);
 }
 
 }  // namespace
 
-size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim) {
-  return (size_t)plan_of(tokens, hc, dim).blocks * hc * dim * sizeof(float);
+size_t engram_gate_grad_workspace(bool f32, int64_t tokens, int32_t hc, int32_t dim) {
+  return (size_t)plan_of(f32, tokens, hc, dim).blocks * hc * dim * sizeof(float);
 }
 
 hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
@@ -554,7 +563,7 @@ hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int3
   a.eps = eps;
   a.clamp = clamp;
   a.plain = plain;
-  const GateGradPlan p = plan_of(tokens, hc, dim);
+  const GateGradPlan p = plan_of(g.f32, tokens, hc, dim);
 #define ENGRAM_GATE_GRAD(F)                                                 \
   if (g.kv_i8 && g.h_i8) launch<F, true, true>(a, p, stream); \
   else if (g.kv_i8) launch<F, true, false>(a, p, stream);     \

@@ -159,7 +159,7 @@ hipError_t engram_launch_gemm_i8(const int8_t *w_codes, const float *w_scales, c
                                  int64_t k, hipStream_t stream);
 
 // The gate's gradient; the workspace holds engram_gate_grad_workspace bytes.
-size_t engram_gate_grad_workspace(int64_t tokens, int32_t hc, int32_t dim);
+size_t engram_gate_grad_workspace(bool f32, int64_t tokens, int32_t hc, int32_t dim);
 hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
                                    float eps, float clamp, int plain, hipStream_t stream);
 

@@ -121,70 +121,80 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 
 // A row in the registers of TEAM threads (a wave, or the block), CPT groups of 8 a thread.
 // src and values may be the same buffer (each value is read and written by one thread), so
-// neither is marked restrict.
+// neither is marked restrict. The grid walks the rows.
 template <bool F32, bool VEC, bool POW2, int TEAM, int CPT>
 __global__ __launch_bounds__(kThreads) void quantize_i8_kernel(const void *src, int64_t rows, int64_t cols,
                                                                int64_t ld, int64_t out_cols,
                                                                uint2 *__restrict__ codes,
                                                                float *__restrict__ scales, void *values) {
-  const int64_t row = TEAM == 64 ? (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6) : blockIdx.x;
-  const int at = TEAM == 64 ? threadIdx.x & 63 : threadIdx.x;
-  if (TEAM == 64 && row >= rows) return;
+  constexpr int kTeams = kThreads / TEAM;
+  __shared__ uint32_t red[2][kThreads / 64];
+  const int at = threadIdx.x % TEAM;
   const int64_t groups = out_cols / 8;
-  Eight<F32, VEC> x[CPT];
-  uint32_t top = 0;
+  int slot = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; row < rows;
+       row += (int64_t)gridDim.x * kTeams) {
+    Eight<F32, VEC> x[CPT];
+    uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) x[i].load(src, row * ld, (int64_t)(at + i * TEAM) * 8, cols);
+    for (int i = 0; i < CPT; ++i) x[i].load(src, row * ld, (int64_t)(at + i * TEAM) * 8, cols);
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) top = max(top, x[i].top());
-  top = wave_max(top);
-  if (TEAM != 64) {
-    __shared__ uint32_t red[kThreads / 64];
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-    __syncthreads();
+    for (int i = 0; i < CPT; ++i) top = max(top, x[i].top());
+    top = wave_max(top);
+    if (TEAM != 64) {
+      // the next row's barrier stands between these reads and the writes after it
+      if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = top;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) top = max(top, red[w]);
-  }
-  const RowScale r = row_scale<POW2>(top);
-  if (at == 0) scales[row] = r.scale;
+      for (int w = 0; w < kThreads / 64; ++w) top = max(top, red[slot][w]);
+      slot ^= 1;
+    }
+    const RowScale r = row_scale<POW2>(top);
+    if (at == 0) scales[row] = r.scale;
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int64_t g = at + i * TEAM;
-    if (g >= groups) break;
-    const uint2 w = x[i].template encode<POW2>(r);
-    codes[row * groups + g] = w;
-    if (values != nullptr) x[i].store(values, row * ld, g * 8, cols, r.scale);
+    for (int i = 0; i < CPT; ++i) {
+      const int64_t g = at + i * TEAM;
+      if (g >= groups) break;
+      const uint2 w = x[i].template encode<POW2>(r);
+      codes[row * groups + g] = w;
+      if (values != nullptr) x[i].store(values, row * ld, g * 8, cols, r.scale);
+    }
   }
 }
 
 // A longer row: read twice, the second time from L2.
 template <bool F32, bool VEC, bool POW2>
-__global__ __launch_bounds__(kLongThreads) void quantize_i8_long_kernel(const void *src, int64_t cols,
-                                                                        int64_t ld, int64_t out_cols,
+__global__ __launch_bounds__(kLongThreads) void quantize_i8_long_kernel(const void *src, int64_t rows,
+                                                                        int64_t cols, int64_t ld,
+                                                                        int64_t out_cols,
                                                                         uint2 *__restrict__ codes,
                                                                         float *__restrict__ scales,
                                                                         void *values) {
-  __shared__ uint32_t red[kLongThreads / 64];
-  const int64_t row = blockIdx.x, groups = out_cols / 8;
-  Eight<F32, VEC> x;
-  uint32_t top = 0;
+  __shared__ uint32_t red[2][kLongThreads / 64];
+  const int64_t groups = out_cols / 8;
+  int slot = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    Eight<F32, VEC> x;
+    uint32_t top = 0;
 #pragma unroll 4
-  for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
-    x.load(src, row * ld, g * 8, cols);
-    top = max(top, x.top());
-  }
-  top = wave_max(top);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-  __syncthreads();
+    for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
+      x.load(src, row * ld, g * 8, cols);
+      top = max(top, x.top());
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = top;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kLongThreads / 64; ++w) top = max(top, red[w]);
-  const RowScale r = row_scale<POW2>(top);
-  if (threadIdx.x == 0) scales[row] = r.scale;
-  for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
-    x.load(src, row * ld, g * 8, cols);
-    const uint2 w = x.template encode<POW2>(r);
-    codes[row * groups + g] = w;
-    if (values != nullptr) x.store(values, row * ld, g * 8, cols, r.scale);
+    for (int w = 0; w < kLongThreads / 64; ++w) top = max(top, red[slot][w]);
+    slot ^= 1;
+    const RowScale r = row_scale<POW2>(top);
+    if (threadIdx.x == 0) scales[row] = r.scale;
+    for (int64_t g = threadIdx.x; g < groups; g += kLongThreads) {
+      x.load(src, row * ld, g * 8, cols);
+      const uint2 w = x.template encode<POW2>(r);
+      codes[row * groups + g] = w;
+      if (values != nullptr) x.store(values, row * ld, g * 8, cols, r.scale);
+    }
   }
 }
 
@@ -193,9 +203,12 @@ __global__ __launch_bounds__(kLongThreads) void quantize_i8_long_kernel(const vo
 template <bool F32, bool VEC, bool POW2>
 void launch(const void *src, int64_t rows, int64_t cols, int64_t ld, int64_t out_cols, uint2 *codes,
             float *scales, void *values, hipStream_t stream) {
+  // at most 2^32 threads to a launch
+  const int64_t most = (int64_t)1 << 21, teams = out_cols <= 1024 ? kThreads / 64 : 1;
+  const int64_t blocks = (rows + teams - 1) / teams;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most));
 #define ENGRAM_QUANTIZE(T, C)                                                                   \
-  hipLaunchKernelGGL((quantize_i8_kernel<F32, VEC, POW2, T, C>),                                \
-                     dim3((unsigned)(T == 64 ? (rows + 3) / 4 : rows)), dim3(kThreads), 0, stream, src, \
+  hipLaunchKernelGGL((quantize_i8_kernel<F32, VEC, POW2, T, C>), grid, dim3(kThreads), 0, stream, src, \
                      rows, cols, ld, out_cols, codes, scales, values)
   if (out_cols <= 512) ENGRAM_QUANTIZE(64, 1);
   else if (out_cols <= 1024) ENGRAM_QUANTIZE(64, 2);
@@ -204,8 +217,8 @@ void launch(const void *src, int64_t rows, int64_t cols, int64_t ld, int64_t out
   else if (out_cols <= 6144) ENGRAM_QUANTIZE(kThreads, 3);
   else if (out_cols <= 8192) ENGRAM_QUANTIZE(kThreads, 4);
   else
-    hipLaunchKernelGGL((quantize_i8_long_kernel<F32, VEC, POW2>), dim3((unsigned)rows), dim3(kLongThreads), 0,
-                       stream, src, cols, ld, out_cols, codes, scales, values);
+    hipLaunchKernelGGL((quantize_i8_long_kernel<F32, VEC, POW2>), grid, dim3(kLongThreads), 0, stream, src, rows,
+                       cols, ld, out_cols, codes, scales, values);
 #undef ENGRAM_QUANTIZE
 }
 

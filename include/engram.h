@@ -229,6 +229,7 @@ typedef struct engram_embed_desc {
 
 #define ENGRAM_MAX_I8_IN_DIM 131056  /* in_dim of the 8-bit products: sums below 2^31 */
 #define ENGRAM_MAX_GRAD_OUT_DIM (1ll << 23) /* out_dim of engram_project_grad       */
+#define ENGRAM_MAX_GRAD_TOKENS (1ll << 30)  /* its tokens                          */
 
 /*
  * What engram_gate_grad computes from: kv and h (before the update) of
@@ -903,7 +904,8 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
  *   e_scales  float [tokens], 16-byte aligned
  *   grad      grad_type [out_dim, in_dim], 16-byte aligned; accumulate 1: the sums are
  *             added to it, 0: it is overwritten (with zeros for no tokens)
- *   in_dim, out_dim, tokens  as engram_project_i8; out_dim <= ENGRAM_MAX_GRAD_OUT_DIM
+ *   in_dim, out_dim, tokens  as engram_project_i8; out_dim <= ENGRAM_MAX_GRAD_OUT_DIM,
+ *             tokens <= ENGRAM_MAX_GRAD_TOKENS
  *   workspace NULL, or at least engram_project_grad_workspace_size bytes, 256-byte
  *             aligned: calls with fewer output tiles than the GPU has CUs then split
  *             the tokens over them, with fp32 parts summed in a fixed order

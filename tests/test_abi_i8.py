@@ -76,6 +76,12 @@ def test_products_refuse_shapes(kw, status):
                                                                             ("out_dim", 64))]) == 0
 
 
+def test_weight_gradient_refuses_sizes_beyond_its_offsets():
+    assert _weight_grad(out_dim=E.MAX_GRAD_OUT_DIM + 8, in_dim=16) == E.ESHAPE
+    assert _weight_grad(tokens=E.MAX_GRAD_TOKENS + 1, in_dim=16, out_dim=8) == E.ESHAPE
+    assert E.engram_project_grad_workspace_size(E.MAX_GRAD_TOKENS + 1, 16, 8) == 0
+
+
 def test_products_refuse_types_pointers_and_workspaces():
     for t in (E.I8, -1):
         assert _project(kv_type=t) == E.EINVAL

@@ -184,6 +184,20 @@ def test_quantize_offsets_beyond_32_bits():
     assert int(codes[:-3].abs().max()) == 0 and float(scales[:-3].abs().max()) == 0.0
 
 
+def test_quantize_more_rows_than_a_launch_has_waves():
+    say("quantize_i8: many rows")
+    for rows, cols in (((1 << 23) + 5, 16), ((1 << 21) + 3, 1040)):
+        src = torch.zeros((rows, cols), dtype=torch.bfloat16, device=DEV)
+        g = torch.Generator(device=DEV).manual_seed(2)
+        src[-7:] = torch.randn((7, cols), generator=g, device=DEV).to(torch.bfloat16)
+        codes, scales, values = quantize(src, cols)
+        ec, es, ev = quantize_reference(src[-7:].double().cpu().numpy(), cols, E.SCALE_F32)
+        np.testing.assert_array_equal(codes[-7:].cpu().numpy(), ec)
+        np.testing.assert_array_equal(scales[-7:].cpu().numpy(), es)
+        assert int(codes[:-7].abs().max()) == 0 and float(scales[:-7].abs().max()) == 0.0
+        assert float(values[:-7].abs().max()) == 0.0
+
+
 # ---- the product -------------------------------------------------------------------
 
 def codes_of(rows, cols, seed, full=False):

@@ -157,7 +157,9 @@ def check_gate(case, **kw):
 
 @pytest.mark.parametrize("fmt,kv,h", [(f, kv, h) for f in (E.BF16, E.F32) for kv in (f, E.I8) for h in (f, E.I8)])
 @pytest.mark.parametrize("tokens,hc,dim", [(1, 1, 8), (1, 4, 5120), (3, 2, 24), (7, 4, 64), (64, 1, 64), (130, 3, 520),
-                                           (517, 4, 136), (1100, 2, 1000), (40, 8, 1024), (9, 5, 8192), (700, 4, 512)])
+                                           (517, 4, 136), (1100, 2, 1000), (40, 8, 1024), (9, 5, 8192), (700, 4, 512),
+                                           (2100, 8, 64), (600, 6, 2048), (33, 7, 3656), (300, 5, 4096), (5, 4, 6400),
+                                           (1300, 2, 2056), (90, 3, 4616), (2, 8, 8192), (1500, 8, 32)])
 def test_gate_gradient(tokens, hc, dim, fmt, kv, h):
     say("gate_grad", tokens, hc, dim, fmt, kv, h)
     check_gate(Case(tokens, hc, dim, fmt, kv, h, seed=tokens + dim))
@@ -442,6 +444,26 @@ def test_weight_gradient_added_to_bf16():
     plain = weight_grad(*case, E.F32)
     got = weight_grad(*case, E.BF16, accumulate=1, grad=base)
     assert torch.equal(got, (plain + base.float()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("t", [300, 1500])
+def test_weight_gradient_added_across_splits(t):
+    """Few tiles and many tokens: with a workspace the tokens are split and joined. Whole
+    numbers, so that every order gives the same."""
+    say("project_grad: splits added to what is there", t)
+    g = torch.Generator(device=DEV).manual_seed(t)
+    k, n = 272, 136
+    d = torch.randint(-3, 4, (t, n), generator=g, device=DEV).to(torch.bfloat16)
+    codes = torch.randint(-20, 21, (t, k), generator=g, device=DEV, dtype=torch.int16).to(torch.int8)
+    one = torch.ones(t, device=DEV)
+    assert E.engram_project_grad_workspace_size(t, k, n) > 0
+    base = torch.randint(-100, 100, (n, k), generator=g, device=DEV).float()
+    want = d.double().t().contiguous() @ codes.double() + base.double()
+    for workspace in (True, False):
+        got = weight_grad(d, codes, one, E.F32, accumulate=1, grad=base, workspace=workspace)
+        assert torch.equal(got.double(), want)
+        got = weight_grad(d, codes, one, E.BF16, accumulate=1, grad=base.to(torch.bfloat16), workspace=workspace)
+        assert torch.equal(got, want.to(torch.bfloat16))
 
 
 def test_weight_gradient_of_no_tokens():
