@@ -38,6 +38,8 @@ struct GateGradArgs {
   int plain;
 };
 
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
 // Eight consecutive saved values: a chunk of floats, or 8 codes.
 template <bool I8, bool F32>
 struct Saved8 {
@@ -172,7 +174,9 @@ __device__ __forceinline__ void store_dead(const GateGradArgs &a, int64_t t, int
 // Up to HC streams, whose numbers of one token a thread holds together: one barrier a
 // token, and the loads of the next token's stream m are issued as soon as this one's are
 // used up, so that a token is in flight while another is worked on. The learned scales lie
-// in LDS as w = q_w k_w rounded to fp32 and what that drops, rounded to bf16. A block has
+// in LDS as w = q_w k_w rounded to fp32 and the part of it that this drops, 2^24 times that in
+// fp16: 36 bits in all (bf16 left dq_w of 32768 x 4 x 5120 off by 1.3e-6 of its norm where one
+// token's s came near 0, against 2e-7). A block has
 // `teams` teams of `width` threads, each on a token of its own, which share w; their parts
 // of dw meet in LDS at the end. F32: fp32 streams, else bf16. KI8, HI8: keys and value,
 // streams as codes.
@@ -215,20 +219,23 @@ __global__ __launch_bounds__(token_threads(F32, HC)) void gate_grad_token_kernel
   }
   v.load(a.kv, begin * (hc + 1) + hc, a.dim, ci);
   float *w_hi = reinterpret_cast<float *>(w_lds);
-  uint16_t *w_lo = reinterpret_cast<uint16_t *>(w_lds + (size_t)hc * a.dim * 4);
+  f16x8 *w_lo = reinterpret_cast<f16x8 *>(w_lds + (size_t)hc * a.dim * 4);
 #pragma unroll 4
   for (int c = tid; c < hc * cps; c += blockDim.x) {
     engram::Chunk8<true> q, k;
     q.load(a.q_w, c);
     k.load(a.k_w, c);
-    float hi[8], lo[8];
+    float hi[8];
+    f16x8 lo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       hi[e] = q[e] * k[e];
-      lo[e] = fmaf(q[e], k[e], -hi[e]);
+      // at most 1 for normal numbers; others have nothing to add
+      const float part = fmaf(q[e], k[e], -hi[e]) / hi[e] * 16777216.f;
+      lo[e] = (_Float16)(fabsf(part) <= 1.f ? part : 0.f);
     }
     engram::Chunk8<true>::store(w_hi, c, hi);
-    engram::Chunk8<false>::store(w_lo, c, lo);
+    w_lo[c] = lo;
   }
   __syncthreads();
   int slot = 0;
@@ -252,11 +259,10 @@ __global__ __launch_bounds__(token_threads(F32, HC)) void gate_grad_token_kernel
           shh[x] = skk[x] = sdv[x] = 0.f;
           dot[x] = 0.0;
           if (m < hc && on) {
-            float rest = 0.f;
+            float rest = 0.f, low = 0.f;
             engram::Chunk8<true> w;
-            engram::Chunk8<false> lo;
             w.load(w_hi, m * cps + ci);
-            lo.load(w_lo, m * cps + ci);
+            const f16x8 lo = w_lo[m * cps + ci];
             shh[x] = h[m].squares();
             skk[x] = k[m].squares();
 #pragma unroll
@@ -264,16 +270,18 @@ __global__ __launch_bounds__(token_threads(F32, HC)) void gate_grad_token_kernel
               const float he = h[m][e], ke = k[m][e];
               sdv[x] = fmaf(d[m][e], v[e], sdv[x]);
               if (kExact) {
-                // p (w + lo) in three parts: the rounded product, its error and p lo
+                // p q_w k_w in three parts: p w rounded, its error, and what w drops
                 const float p = he * ke, r = p * w[e];
                 rest += fmaf(p, w[e], -r);
-                rest = fmaf(p, lo[e], rest);
+                low = fmaf(r, (float)lo[e], low);
                 dot[x] += (double)r;
               } else {
-                dot[x] = fma((double)he * (double)ke, (double)w[e] + (double)lo[e], dot[x]);
+                const double r = (double)he * (double)ke * (double)w[e];
+                dot[x] += r;
+                low = fmaf((float)r, (float)lo[e], low);
               }
             }
-            dot[x] += (double)rest;
+            dot[x] += (double)rest + (double)low * 0x1p-24;
           }
         }
         const float a0 = sums_of(shh), a1 = sums_of(skk), a2 = sums_of(sdv);
