@@ -2,6 +2,13 @@
 // exact in 32 bits (in_dim < 2^17 codes of at most 128); it is converted to fp32, scaled
 // by the channel, then by the token, and rounded to kv's type.
 //
+// Few tokens are bound by W's stream: 1 token against 25600 rows of 6144 takes 27 us (5.8
+// TB/s), 256 tokens 52 us, of which the loads alone take about 40. Many tokens are bound by
+// power: 32768 tokens take 4.5 ms, 2.3 POPS at 1.8-2.0 GHz with the matrix units 53-59 % busy.
+// The same kernel without its loads reaches 3.1 POPS, MFMAs alone 3.3 (4.3 where every code
+// is zero), and with all loads served by L2 2.5; a ring of four half steps, a deeper prefetch,
+// was no faster.
+//
 // v_mfma_i32_32x32x32_i8 takes 16 bytes a lane: lane l holds row l % 32, inputs [16 h, 16 h +
 // 16) of the 32 for its half h = l / 32. A sum over the inputs may take them in any order
 // that both operands share: of the 128 inputs of a K-step, half h of a wave takes 16-byte
@@ -267,12 +274,18 @@ void i8_wide_kernel(I8Operands op, void *__restrict__ kv, int tiles_m, int tiles
 // the loads issued, those of the R - 2 steps behind it may be outstanding. Every step
 // issues the same number of loads, and steps are rounded up to a multiple of R with steps
 // of zeros, so the count holds throughout.
+//
+// ONCE: one block holds all tokens, so that W's rows are read by one block alone and are
+// marked nontemporal, which leaves L2 to e (1 token 30.4 -> 27.1 us, 256 tokens 55.5 -> 53.1;
+// where two blocks share them 55.7 -> 57.7).
+constexpr int kNontemporal = 2;            // of a buffer load's cache policy
+
 template <int NB, int MT>
 constexpr int ring_of() {
   return NB + MT <= 3 ? 6 : NB + MT <= 4 ? 4 : 3;
 }
 
-template <bool F32, int NB, int MT, int WV>
+template <bool F32, int NB, int MT, int WV, bool ONCE>
 __global__ __launch_bounds__(64 * WV) __attribute__((amdgpu_waves_per_eu(WV / 4, WV / 4)))
 void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
   constexpr int NI = NB * 4 / WV;
@@ -317,7 +330,7 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
         (i & 1) ? e_v1 : e_v0, i * 8 * ld + (kt_) * kStep, 0, 0);                              \
     _Pragma("unroll") for (int i = 0; i < kLW; ++i) __builtin_amdgcn_raw_ptr_buffer_load_lds( \
         rsW, I8_LDS(&IK_SLOT(u)[(wave * kLW + i) * 1024]), 16, (i & 1) ? wv1_ : wv0_,       \
-        i * 8 * ld + (kt_) * kStep, 0, 0);                                                     \
+        i * 8 * ld + (kt_) * kStep, 0, ONCE ? kNontemporal : 0);                               \
   }
 #define IK_FRAGS(u, s, fa, fb)                                                                 \
   _Pragma("unroll") for (int i = 0; i < NI; ++i)                                               \
@@ -411,16 +424,25 @@ void i8_skinny_kernel(I8Operands op, void *__restrict__ kv, int tiles_n) {
 #undef IK_SLOT
 }
 
-template <bool F32, int NI, int MT, int WV = 4>
+template <bool F32, int NB, int MT, int WV>
 hipError_t launch_skinny(const I8Operands &op, void *kv, hipStream_t stream) {
-  const int tiles_n = (op.N + 64 * NI - 1) / (64 * NI), tiles_m = (op.M + 64 * MT - 1) / (64 * MT);
-  hipLaunchKernelGGL((i8_skinny_kernel<F32, NI, MT, WV>), dim3((unsigned)(tiles_n * tiles_m)), dim3(64 * WV), 0,
-                     stream, op, kv, tiles_n);
+  const int tiles_n = (op.N + 64 * NB - 1) / (64 * NB), tiles_m = (op.M + 64 * MT - 1) / (64 * MT);
+  const dim3 grid((unsigned)(tiles_n * tiles_m)), block(64 * WV);
+  if (tiles_m == 1)
+    hipLaunchKernelGGL((i8_skinny_kernel<F32, NB, MT, WV, true>), grid, block, 0, stream, op, kv, tiles_n);
+  else
+    hipLaunchKernelGGL((i8_skinny_kernel<F32, NB, MT, WV, false>), grid, block, 0, stream, op, kv, tiles_n);
   return hipGetLastError();
 }
 
-// The smallest tile whose blocks fit the CUs at once, else whole 256 x 256 tiles unless
-// their rounds of blocks on the CUs take longer than those of 128 x 256.
+// The smallest tile whose blocks fit the CUs at once: a larger one leaves CUs idle and, at few
+// tokens, multiplies padding. Where none fits, the blocks come in rounds, a round of whole 256 x
+// 256 tiles as long as 1.3 to 1.9 of 128 x 256: those are taken where their rounds number up
+// to 5 / 3 of the whole tiles' (us, 6144 inputs, 128 x 256 against 256 x 256; 1 round to 1:
+// 300 x 20480 48, 73; 2 to 2: 128 x 66048 116, 172 and 600 x 25600 95, 146; 3 to 2: 768 x 25600
+// 128, 153 and 4096 x 5120 158, 172; 2 to 1: 256 x 33024 96, 77 and 300 x 25600 76, 77; 4 to 2:
+// 1003 x 25600 170, 156; 7 to 4: 2048 x 25600 362, 359). From 129 to 256 tokens they are 256
+// tokens by 128 rows, as many blocks, so that W is read once.
 template <bool F32>
 hipError_t launch_i8(const I8Operands &op, void *kv, hipStream_t stream) {
   int cus = 0;
@@ -430,10 +452,12 @@ hipError_t launch_i8(const I8Operands &op, void *kv, hipStream_t stream) {
     const int64_t blocks = ((int64_t)op.M + toks - 1) / toks * (((int64_t)op.N + rows - 1) / rows);
     return (blocks + cus - 1) / cus;
   };
-  if (rounds(64, 64) == 1) return launch_skinny<F32, 1, 1>(op, kv, stream);
-  if (rounds(64, 128) == 1) return launch_skinny<F32, 2, 1>(op, kv, stream);
+  if (rounds(64, 64) == 1) return launch_skinny<F32, 1, 1, 4>(op, kv, stream);
+  if (rounds(64, 128) == 1) return launch_skinny<F32, 2, 1, 4>(op, kv, stream);
   if (rounds(128, 128) == 1) return launch_skinny<F32, 2, 2, 8>(op, kv, stream);
-  if (3 * rounds(128, 256) <= 5 * rounds(BM, BN)) return launch_skinny<F32, 4, 2, 8>(op, kv, stream);
+  if (3 * rounds(128, 256) <= 5 * rounds(BM, BN))
+    return op.M <= 256 && op.M > 128 ? launch_skinny<F32, 2, 4, 8>(op, kv, stream)
+                                     : launch_skinny<F32, 4, 2, 8>(op, kv, stream);
   const int tiles_m = (op.M + BM - 1) / BM, tiles_n = (op.N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   hipLaunchKernelGGL((i8_wide_kernel<F32>), dim3((unsigned)(tiles > cus ? cus : tiles)), dim3(kWideThreads),
