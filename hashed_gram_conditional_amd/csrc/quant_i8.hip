@@ -1,6 +1,20 @@
 // Quantisation to 8-bit integers with one scale per row (engram_quantize_i8): s = amax /
 // 127 rounded to fp32, or the smallest power of two with amax <= 127 s, and codes x
 // (127 / amax) or x / s, to the nearest whole number, ties to the even one.
+//
+// A code is that of the exact product with the fp32 factor: the fp32 product decides it
+// unless it falls on a half, where its rounding error says on which side the exact one lies.
+// The row's maximum is taken on the values' bits (as integers, where infinities and NaN lie
+// above every finite value). A bf16 value q s is rounded to fp32 first, which gives the
+// bf16 number that one rounding would: amax is a bf16 number then, A 2^e with A < 2^8, and q A /
+// 127 is the middle of two bf16 numbers or at least 2^-16 of itself away from one, because
+// 2^j q A and 127 times an odd number, both below 2^16, differ by 1 or more; and in the middle
+// q or A is a multiple of 127, and q s is exact or amax.
+//
+// One pass, bound by HBM: a row waits for its maximum in the registers of a wave (up to 1024
+// columns) or a block (up to 8192). 25600 x 6144 fp32 with values take 280 us (1.42 GB, 5.1
+// TB/s), 40960 x 5120 bf16 with values 180 us (1.05 GB, 5.8 TB/s), 256 x 6144 bf16 5.8 us.
+// Rows read value by value, twice, took 453, 516 and 9.5 us.
 #include "common.h"
 
 namespace {

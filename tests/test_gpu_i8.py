@@ -27,6 +27,13 @@ def bf16_round(x):
     return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(torch.bfloat16).float().numpy()
 
 
+def bf16_once(x):
+    """float64 -> nearest bf16 as float64, by its 8 leading bits (normal numbers only; a
+    conversion by way of float32 would round twice)."""
+    part, exp = np.frexp(x)
+    return np.ldexp(np.rint(part * 256) / 256, exp)
+
+
 def quantize_reference(x, out_cols, kind):
     """Codes, scales (float32) and exact values (float64) of float64 rows by the definition.
     x times an fp32 factor has at most 48 bits and is exact in float64."""
@@ -77,8 +84,8 @@ def check_quantize(x, cols, ld=0, out_cols=None, kind=E.SCALE_F32):
     ec, es, ev = quantize_reference(x[:, :cols].double().numpy(), codes.shape[1], kind)
     np.testing.assert_array_equal(scales.cpu().numpy(), es)
     np.testing.assert_array_equal(codes.cpu().numpy(), ec)
-    # q s has 8 + 24 bits: exact in float64, rounded once by the conversion
-    want = torch.from_numpy(ev).to(x.dtype).double().numpy()
+    # q s has 8 + 24 bits: exact in float64, rounded once
+    want = ev.astype(np.float32).astype(np.float64) if x.dtype == torch.float32 else bf16_once(ev)
     got = values.cpu().double().numpy()
     np.testing.assert_array_equal(got[:, :cols], want)
     assert (got[:, cols:] == 9.0).all()
