@@ -25,6 +25,7 @@ constexpr uint32_t kSmallest = 8u << 23;      // 2^-119
 
 struct RowScale {
   float scale, inv;
+  float most;               // of a code's magnitude
   bool bad;
 };
 
@@ -33,6 +34,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   RowScale r;
   r.bad = top >= 0x7F800000u;
   r.scale = r.inv = 0.f;
+  r.most = 127.f;
   if (r.bad) {
     r.scale = __uint_as_float(0x7FC00000u);
   } else if (top >= kSmallest) {
@@ -41,6 +43,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
       const uint32_t field = (top >> 23) - 6 + ((top & 0x7FFFFFu) > 0x7E0000u);
       r.scale = __uint_as_float(field << 23);
       r.inv = __uint_as_float((254u - field) << 23);
+      if (field == 249u) r.most = 63.f;      // 64 steps of 2^122 would not be finite
     } else {
       const float amax = __uint_as_float(top);
       r.scale = amax / 127.f;
@@ -100,7 +103,9 @@ struct Eight {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       // x / s is exact where s is a power of two
-      f[e] = r.bad ? 0.f : POW2 ? rintf(f[e] * r.inv) : code_of(f[e], r.inv);
+      f[e] = r.bad ? 0.f
+             : POW2 ? fminf(fmaxf(rintf(f[e] * r.inv), -r.most), r.most)
+                    : code_of(f[e], r.inv);
       w[e / 4] |= ((uint32_t)(int)f[e] & 0xFFu) << (8 * (e % 4));
     }
     return make_uint2(w[0], w[1]);

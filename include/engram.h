@@ -816,7 +816,8 @@ size_t engram_project_mx4_workspace_size(int64_t tokens, int64_t in_dim, int64_t
 /*
  * Quantisation to 8-bit integers with one scale per row: for a row of largest
  * magnitude amax the scale s of scale_kind and the codes q, x (127 / amax rounded to
- * fp32) or x / s to the nearest whole number (ties to even), so |q| <= 127. A row with
+ * fp32) or x / s to the nearest whole number (ties to even), so |q| <= 127 (at most 63
+ * where s = 2^122, so that q s is finite). A row with
  * amax < 2^-119 counts as zeros and gets scale 0; a row that holds an infinity or a NaN
  * gets scale NaN and zero codes. It serves activations (a row per token), weights (a row
  * per output channel) and checkpoints of either.

@@ -60,6 +60,8 @@ def quantize_reference(x, out_cols, kind):
                 s = np.nextafter(s, np.float32(0))
         scales[r] = s
         codes[r, :cols] = np.rint(x[r] * by)
+        if 64 * float(s) > float(np.finfo(np.float32).max):
+            codes[r] = np.clip(codes[r], -63, 63)
         values[r] = codes[r, :cols] * float(s)
     return codes, scales, values
 
