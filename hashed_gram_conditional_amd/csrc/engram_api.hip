@@ -1348,6 +1348,7 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
     return ENGRAM_EINVAL;
   if (q_w == nullptr || k_w == nullptr) return ENGRAM_EINVAL;
   const int64_t ntok = desc->batch * desc->seq;
+  if (ntok == 0 && (d_q_w == nullptr || accumulate)) return ENGRAM_OK;
   if (ntok > 0) {
     if (ids == nullptr || saved->kv == nullptr || saved->h == nullptr || d_out == nullptr ||
         d_h == nullptr || d_kv == nullptr || (kv_i8 && saved->kv_scales == nullptr) ||

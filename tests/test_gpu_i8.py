@@ -99,7 +99,9 @@ def check_quantize(x, cols, ld=0, out_cols=None, kind=E.SCALE_F32):
     (1, 1, 0, 16), (1, 16, 0, 16), (3, 15, 0, 48), (5, 17, 24, 64), (7, 128, 0, 256), (2, 1001, 1003, 1024),
     (257, 96, 104, 96), (300, 64, 0, 64), (33, 6144, 0, 6144), (4, 1000, 1000, 1152), (130, 8, 0, 128),
     (5, 512, 0, 512), (6, 520, 0, 528), (3, 2048, 0, 2048), (3, 4104, 0, 4112), (2, 8192, 8195, 8192),
-    (2, 8200, 0, 8208), (2, 20001, 0, 20016), (1, 131072, 0, 131072)])
+    (2, 8200, 0, 8208), (2, 20001, 0, 20016), (1, 131072, 0, 131072),
+    (41, 63, 0, 64), (77, 100, 101, 112), (19, 127, 129, 128), (23, 250, 0, 256), (50, 255, 255, 256),
+    (100, 511, 513, 512), (9, 1023, 0, 1024), (6, 2047, 2049, 2048), (5, 6143, 6143, 6144), (1000, 24, 26, 32)])
 def test_quantize_against_the_definition(kind, st, rows, cols, ld, out_cols):
     say("quantize_i8", kind, st, rows, cols, ld, out_cols)
     g = torch.Generator().manual_seed(rows + cols)
@@ -269,10 +271,10 @@ def test_project_step_counts(m, n, k):
     check_project(m, k, n, E.F32, seed=k)
 
 
+@pytest.mark.parametrize("k", [16, 144, 400])
 @pytest.mark.parametrize("m,n", [(1, 25600), (256, 25600), (600, 5120), (1003, 25600), (2048, 12288)])
-def test_project_wide(m, n):
-    say("project_i8: wide", m, n)
-    k = 400
+def test_project_wide(m, n, k):
+    say("project_i8: wide", m, n, k)
     e, w = codes_of(m, k, 1), codes_of(n, k, 2)
     es, ws = scales_of(m, 3), scales_of(n, 4)
     want = torch.from_numpy(project_reference(e, es, w, ws)).to(torch.bfloat16)
