@@ -1,16 +1,16 @@
 // Gradient of the projection's weight from 8-bit codes of its inputs: dW[n, k] = sum_t
 // d_kv[t, n] s_t q[t, k], in the bf16 MFMA with fp32 sums. s_t q[t, k] is rounded to bf16, as
 // d_kv is: s_t belongs to the summed index, so it cannot wait for the sum, and the rounding
-// (2^-9 of a value whose code is a whole number below 128) is small beside the quantiser's.
+// (at most 2^-8 of a value whose code is a whole number below 128) is small beside the quantiser's.
 //
 // Both operands have the summed index outermost, the MFMA reads it innermost. The kernel turns
 // them on the way through registers, where the codes have to pass anyway. Other ways measured
 // at 32768 x 25600 x 6144: LDS reads that transpose (ds_read_b64_tr_b16; half the rate of
 // 16-byte reads, 2650 cycles of LDS a step beside 2048 of the MFMAs) 10.0 ms; the codes scaled
-// and turned by a launch before, direct loads of them here, 10.0 ms; this 9.3-9.8 ms, 1.05-1.11
+// and turned by a launch before, direct loads of them here, 10.0 ms; this 9.1-9.4 ms, 1.10-1.13
 // PFLOP/s. It is bound by power: 1.7-1.8 GHz, the matrix units 59 % busy; with codes and
 // gradients of zero the same kernel takes 7.5 ms, and MFMAs with LDS reads alone 6.3 ms.
-// 509 tokens take 228 us into fp32 (629 MB of gradients), of which each of the ten rounds of
+// 509 tokens take 223 us into fp32 (629 MB of gradients), of which each of the ten rounds of
 // tiles spends 13 us in its eight steps and 10 us in its first loads and its stores; one block
 // per CU that walks the tiles with the next one's loads ahead saved 2 % there and lost 9 %
 // in the long sum, whose addresses it had to form anew in every step.
@@ -81,10 +81,12 @@ __device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, 
   }
 }
 
-// Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 4 tiles of d_kv's
-// columns by all of e's, so that its 32 blocks share 4 panels of d_kv (512 bytes a token)
-// and 8 of codes (256).
-constexpr int kGroupN = 4;
+// Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 2 tiles of d_kv's
+// columns by all of e's, so that its 32 blocks share 2 panels of d_kv and 16 of codes. By the
+// bytes alone 4 by 8 would be less to read (512 bytes of d_kv a token and 256 of codes), but
+// measured 2 is ahead: 32768 x 25600 x 6144 in 9.18 ms, and 9.19, 9.33 and 9.8 in groups of
+// 1, 4 and 8.
+constexpr int kGroupN = 2;
 
 __device__ __forceinline__ void grad_tile(int bid, int tiles_n, int tiles_k, int &n0, int &k0) {
   const int full = tiles_n * tiles_k / kXcds * kXcds;
