@@ -142,12 +142,13 @@ __device__ __forceinline__ StreamGrad stream_grad(const GateGradArgs &a, float s
   const float D = (float)(dot * (double)sh * (double)sk);
   const float norm = rh * rk / sqrtf((float)a.dim);
   const float s = D * norm;
-  const float root = sqrtf(fmaxf(fabsf(s), a.clamp));
+  // a NaN stays one, so that no gradient looks sound that a broken saved row went into
+  const float root = sqrtf(fabsf(s) < a.clamp ? a.clamp : fabsf(s));
   const float z = a.plain ? s : copysignf(root, s);
   // alpha (1 - alpha) without the difference of two near ones
   const float small = expf(-fabsf(z));
   float slope = small / ((1.f + small) * (1.f + small));
-  if (!a.plain) slope = fabsf(s) > a.clamp ? slope / (2.f * root) : 0.f;
+  if (!a.plain) slope = fabsf(s) <= a.clamp ? 0.f : slope / (2.f * root);
   const float c1 = sdv * sv * slope * norm;
   StreamGrad g;
   g.alpha = (z < 0.f ? small : 1.f) / (1.f + small);

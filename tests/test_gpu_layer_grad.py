@@ -198,6 +198,28 @@ def test_gate_gradient_dead_rows_may_hold_anything():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("fmt,kv,h", [(E.BF16, E.I8, E.I8), (E.F32, E.I8, E.F32), (E.BF16, E.BF16, E.I8)])
+@pytest.mark.parametrize("hc,dim", [(4, 136), (2, 1000), (5, 8192)])
+def test_gate_gradient_of_rows_that_hold_nan(fmt, kv, h, hc, dim):
+    """At a position that is not DEAD a key that holds a NaN makes the gradients of its stream and of the value
+    NaN, and those of the learned scales; the position's other streams and the other positions keep theirs."""
+    say("gate_grad: NaN in a key", fmt, kv, h, hc, dim)
+    for plain in (False, True):
+        case = Case(60, hc, dim, fmt, kv, h, plain=plain, dead=0.0, seed=17)
+        want = case.run()
+        if kv == E.I8:
+            case.kv_scales[7, 1] = float("nan")
+        else:
+            case.kv[7, 1, 5] = float("nan")
+        d_h, d_kv, d_q, d_k = case.run()
+        assert torch.isnan(d_h[7, 1]).all() and torch.isnan(d_kv[7, 1]).all() and torch.isnan(d_kv[7, hc]).all()
+        assert torch.isnan(d_q[1]).all() and torch.isnan(d_k[1]).all()
+        d_h[7, 1], d_kv[7, 1], d_kv[7, hc] = want[0][7, 1], want[1][7, 1], want[1][7, hc]
+        d_q[1], d_k[1] = want[2][1], want[3][1]
+        for a, b in zip((d_h, d_kv, d_q, d_k), want):
+            assert torch.equal(a, b)
+
+
 def test_gate_gradient_raw_ids_outside_the_vocabulary():
     say("gate_grad: ids")
     case = Case(20, 2, 64, dead=0.0, seed=1)
