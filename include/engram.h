@@ -871,8 +871,11 @@ size_t engram_project_i8_workspace_size(int64_t tokens, int64_t in_dim, int64_t 
  *   d_q_w = k_w sum over the tokens of c1 h k, d_k_w = q_w of the same
  * The signed root's derivative is taken as 0 where |s| <= gate_clamp (at s = 0 with
  * clamp 0 too). A DEAD position passes d_out on, with a zero d_kv row and no part in
- * d_q_w and d_k_w; its saved rows are not used. At another position a NaN in a stream's
- * saved row or scale makes that stream's gradients and the value's NaN.
+ * d_q_w and d_k_w; its saved rows are not used. At another position a NaN in the saved
+ * row or scale of a stream or of its key makes that stream's gradients, the key's and the
+ * value's NaN; one in the value's makes those of every stream and key of the position NaN
+ * (the value's own gradient does not depend on the value). Either reaches d_q_w and d_k_w
+ * of those streams.
  *   desc       as engram_gate: batch, seq, hc, dim, row_format, eps, gate_clamp, gate_mode
  *   ids        int32 [B, T], raw_vocab: as engram_gate
  *   saved      [host] the saved inputs

@@ -242,6 +242,80 @@ def test_gate_gradient_in_place_without_weights_and_added():
     assert torch.equal(c[2], q0 + d_q) and torch.equal(c[3], k0 + d_k)
 
 
+def test_gate_gradient_zero_products_under_a_clamp():
+    """s = 0 with a clamp above 0: the gate is sigmoid(sqrt(clamp)) there, as the forward pass has it,
+    and the root's derivative 0, so that the streams' gradient is d_out and the keys' is 0."""
+    say("gate_grad: s = 0 under a clamp")
+    clamp = 0.04
+    for hc, dim in ((2, 64), (5, 8192)):
+        for kv in (E.BF16, E.I8):
+            case = Case(8, hc, dim, E.BF16, kv, E.BF16, clamp=clamp, dead=0.0, seed=2)
+            zero = [(1, 0), (2, 1), (3, 0)]
+            case.kv[1, 0], case.kv64[1, 0] = 0, 0.0
+            case.h[2, 1], case.h64[2, 1] = 0.0, 0.0
+            case.kv[3, 0], case.kv64[3, 0] = 0, 0.0
+            case.h[3, 0], case.h64[3, 0] = 0.0, 0.0
+            if kv == E.BF16:                       # disjoint halves
+                zero.append((4, 1))
+                case.kv[4, 1, :dim // 2], case.kv64[4, 1, :dim // 2] = 0.0, 0.0
+                case.h[4, 1, dim // 2:], case.h64[4, 1, dim // 2:] = 0.0, 0.0
+            got = check_gate(case)
+            for t, m in zero:
+                assert torch.equal(got["d_h"][t, m], case.d_out[t, m]) and not got["d_kv"][t, m].any()
+            if kv == E.BF16:
+                alpha = torch.empty((8, hc), device=DEV)
+                E.engram_gate(case.desc, case.ids, VOCAB, case.kv, case.q_w, case.k_w, case.h.clone(), alpha)
+                torch.cuda.synchronize()
+                # a root, an exponential of at most 1, a sum and a division
+                want = 1 / (1 + math.exp(-math.sqrt(clamp)))
+                assert all(abs(float(alpha[t, m]) - want) <= 16 * U for t, m in zero)
+
+
+@pytest.mark.parametrize("fmt,kv,h", [(E.BF16, E.I8, E.I8), (E.F32, E.F32, E.I8), (E.BF16, E.BF16, E.BF16)])
+@pytest.mark.parametrize("hc,dim", [(4, 136), (2, 1000), (5, 8192)])
+def test_gate_gradient_of_streams_and_values_that_hold_nan(fmt, kv, h, hc, dim):
+    """A NaN in a stream's saved row or scale does to the gradients what one in its key does. One in
+    the value's row or scale makes those of the position's streams and keys NaN, and the learned scales';
+    the value's own gradient, which does not depend on the value, and the other positions keep theirs."""
+    say("gate_grad: NaN in a stream and in the value", fmt, kv, h, hc, dim)
+    for plain in (False, True):
+        for broken in ("stream", "value"):
+            case = Case(60, hc, dim, fmt, kv, h, plain=plain, dead=0.0, seed=18)
+            want = case.run()
+            if broken == "stream":
+                if h == E.I8:
+                    case.h_scales[7, 1] = float("nan")
+                else:
+                    case.h[7, 1, 5] = float("nan")
+            elif kv == E.I8:
+                case.kv_scales[7, hc] = float("nan")
+            else:
+                case.kv[7, hc, 5] = float("nan")
+            d_h, d_kv, d_q, d_k = case.run()
+            streams = slice(1, 2) if broken == "stream" else slice(0, hc)
+            assert torch.isnan(d_h[7, streams]).all() and torch.isnan(d_kv[7, streams]).all()
+            assert torch.isnan(d_q[streams]).all() and torch.isnan(d_k[streams]).all()
+            d_h[7, streams], d_kv[7, streams] = want[0][7, streams], want[1][7, streams]
+            d_q[streams], d_k[streams] = want[2][streams], want[3][streams]
+            if broken == "stream":
+                assert torch.isnan(d_kv[7, hc]).all()
+                d_kv[7, hc] = want[1][7, hc]
+            for a, b in zip((d_h, d_kv, d_q, d_k), want):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt,kv,h,t,hc,dim", [(E.BF16, E.I8, E.I8, 5000, 4, 136), (E.BF16, E.BF16, E.BF16, 1100, 4, 2056),
+                                               (E.F32, E.I8, E.F32, 1300, 2, 2056), (E.BF16, E.I8, E.BF16, 700, 4, 6400),
+                                               (E.BF16, E.I8, E.I8, 3000, 8, 32)])
+def test_gate_gradient_in_place_over_many_turns(fmt, kv, h, t, hc, dim):
+    """Several tokens a block, of which the next ones' rows are requested before this one's are stored."""
+    say("gate_grad: in place, several tokens a block", fmt, kv, h, t, hc, dim)
+    case = Case(t, hc, dim, fmt, kv, h, dead=0.2, seed=19)
+    want = case.run()
+    for a, b in zip(case.run(in_place=True), want):
+        assert torch.equal(a, b)
+
+
 def test_gate_gradient_of_no_tokens():
     say("gate_grad: no tokens")
     desc = E.forward_desc(2, 0, 2, 64, 0, E.ROW_E4M3_E8M0_264, 256)
