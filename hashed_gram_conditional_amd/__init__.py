@@ -8,7 +8,7 @@ in, raw pointers out). Importing it fails if the library is not built.
 from ._binding import (  # noqa: F401
     DEAD, MAX_NGRAM, MAX_SEGMENTS, MAX_LAYERS, MAX_TOTAL_SEGMENTS, ROW_BYTES, ROW_E4M3_E8M0_264, ROW_F32,
     GATE_SIGNED_SQRT, GATE_PLAIN, MAX_CONV_TAPS, MAX_CONV_HISTORY,
-    BF16, F32, I8, MX_E4M3, MX_E2M1, SCALE_F32, SCALE_POW2, MAX_I8_IN_DIM,
+    BF16, F32, I8, F32_FINE, MX_E4M3, MX_E2M1, SCALE_F32, SCALE_POW2, MAX_I8_IN_DIM,
     MAX_GRAD_OUT_DIM, MAX_GRAD_TOKENS, MAX_EMBED_DIM, MAX_EMBED_GRAD_IDS,
     OK, EINVAL, EVOCAB, EMULT, ESHAPE, EWORKSPACE, EHIP, EPRIMES, ESCRATCH,
     EngramError, HashParams, ForwardDesc, ShortConv, EmbedDesc, GateSaved, LIB, LIB_PATH,

@@ -32,6 +32,7 @@ F32 = 1
 MX_E4M3 = 0
 MX_E2M1 = 1
 I8 = 2
+F32_FINE = 3
 SCALE_F32 = 0
 SCALE_POW2 = 1
 MAX_I8_IN_DIM = 131056
@@ -628,7 +629,8 @@ def engram_project_grad(d_kv, e_codes, e_scales, grad, grad_type: int, accumulat
                         tokens: int, in_dim: int, out_dim: int, workspace=None,
                         workspace_bytes: int = 0, stream=None):
     """The projection weight's gradient from 8-bit codes of its inputs, overwritten (0) or
-    added to (1)."""
+    added to (1); grad_type BF16, F32, or F32_FINE for fp32 from scales that are no powers of
+    two."""
     _check(LIB.engram_project_grad(_ptr(d_kv), _ptr(e_codes), _ptr(e_scales), _ptr(grad), grad_type,
                                    accumulate, tokens, in_dim, out_dim, _ptr(workspace),
                                    workspace_bytes, _stream(stream, grad)), "engram_project_grad")

@@ -1395,7 +1395,8 @@ int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_sc
                         int32_t grad_type, int32_t accumulate, int64_t tokens, int64_t in_dim,
                         int64_t out_dim, void *workspace, size_t workspace_bytes,
                         hipStream_t stream) {
-  if (!float_type_ok(grad_type) || (accumulate != 0 && accumulate != 1)) return ENGRAM_EINVAL;
+  const bool fine = grad_type == ENGRAM_F32_FINE;
+  if (!(float_type_ok(grad_type) || fine) || (accumulate != 0 && accumulate != 1)) return ENGRAM_EINVAL;
   if (!i8_gradient_shape_ok(tokens, in_dim, out_dim)) return ENGRAM_ESHAPE;
   if (tokens == 0 && accumulate) return ENGRAM_OK;
   if (grad == nullptr || (tokens > 0 && (d_kv == nullptr || e_codes == nullptr || e_scales == nullptr)))
@@ -1406,8 +1407,8 @@ int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_sc
   if (workspace != nullptr && (!aligned(workspace, 256) || workspace_bytes < need))
     return ENGRAM_EWORKSPACE;
   return hip_status(engram_launch_gemm_grad((const uint16_t *)d_kv, (const int8_t *)e_codes, e_scales,
-                                            grad_type == ENGRAM_F32, grad, accumulate, tokens,
-                                            out_dim, in_dim,
+                                            grad_type != ENGRAM_BF16, fine, grad, accumulate,
+                                            tokens, out_dim, in_dim,
                                             need > 0 ? (float *)workspace : nullptr, stream));
 }
 

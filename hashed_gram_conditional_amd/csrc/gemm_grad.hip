@@ -1,7 +1,12 @@
 // Gradient of the projection's weight from 8-bit codes of its inputs: dW[n, k] = sum_t
 // d_kv[t, n] s_t q[t, k], in the bf16 MFMA with fp32 sums. s_t q[t, k] is rounded to bf16, as
-// d_kv is: s_t belongs to the summed index, so it cannot wait for the sum, and the rounding
-// (at most 2^-8 of a value whose code is a whole number below 128) is small beside the quantiser's.
+// d_kv is: s_t belongs to the summed index, so it cannot wait for the sum. For codes near 127 the
+// rounding reaches 0.49 of a code step, the quantiser's own half step; in the mean square of normal
+// values whose largest is four standard deviations it is 0.05 of a step beside the quantiser's
+// 0.29, and a gradient is 1.66e-3 of its norm away from that of the unrounded values (4096 and
+// 32768 tokens; powers of two, whose products are bf16 numbers, 1e-7). FINE (ENGRAM_F32_FINE)
+// takes two bf16 terms and twice the MFMAs: 2.5e-6 (sums in fp32 throughout 1.1e-6 and 3.2e-6), in
+// 19.3 ms where one term takes 9.25 (32768 x 25600 x 6144) and 378 us where it takes 229 (509 tokens).
 //
 // Both operands have the summed index outermost, the MFMA reads it innermost. The kernel turns
 // them on the way through registers, where the codes have to pass anyway. Other ways measured
@@ -14,6 +19,8 @@
 // tiles spends 13 us in its eight steps and 10 us in its first loads and its stores; one block
 // per CU that walks the tiles with the next one's loads ahead saved 2 % there and lost 9 %
 // in the long sum, whose addresses it had to form anew in every step.
+#include <type_traits>
+
 #include "gemm_tiles.h"
 
 using namespace engram_gemm;
@@ -27,9 +34,12 @@ struct GradOperands {
   int T, N, K;
 };
 
-constexpr int kStep = 64;                 // tokens per step
+// Tokens per step, whose values of a column fill a row of LDS. FINE: half as many, each of e's
+// values as two bf16 numbers.
+template <bool FINE>
+constexpr int kStep = FINE ? 32 : 64;
 constexpr int kTile = 256;                // columns of either operand
-constexpr int kRow = kStep * 2;           // bytes of a column in LDS
+constexpr int kRow = 128;                 // bytes of a column in LDS
 constexpr int kPatch = 4096;              // LDS of a wave for storing part of its tile
 
 // Stores 32 rows (n) x COLS columns (k, one or two accumulators) of a wave in whole cache
@@ -88,6 +98,27 @@ __device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, 
 // 1, 4 and 8.
 constexpr int kGroupN = 2;
 
+// Two scaled values, as pairs of bf16 numbers: their roundings, and the roundings of what those
+// drop, in all within 2^-17 of the value. A rounding that is not finite has nothing beside it.
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t &high, uint32_t &low) {
+#pragma clang fp contract(off)      // a and b are the rounded products
+  high = engram::pack_bf16x2(a, b);
+  const float x = a - __uint_as_float(high << 16), y = b - __uint_as_float(high & 0xFFFF0000u);
+  low = engram::pack_bf16x2(fabsf(x) < INFINITY ? x : 0.f, fabsf(y) < INFINITY ? y : 0.f);
+}
+
+// Word `at` of a register set, which is a constant where it is unrolled.
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int at) {
+  return at == 0 ? v.x : at == 1 ? v.y : at == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ uint32_t word_of(const uint2 &v, int at) { return at == 0 ? v.x : v.y; }
+__device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
+
+__device__ __forceinline__ uint2 load8(__amdgpu_buffer_rsrc_t rs, int voff, int soff) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0);
+  return make_uint2((uint32_t)v[0], (uint32_t)v[1]);
+}
+
 __device__ __forceinline__ void grad_tile(int bid, int tiles_n, int tiles_k, int &n0, int &k0) {
   const int full = tiles_n * tiles_k / kXcds * kXcds;
   if (bid < full) bid = (bid % kXcds) * (full / kXcds) + bid / kXcds;
@@ -105,7 +136,10 @@ __device__ __forceinline__ void grad_tile(int bid, int tiles_n, int tiles_k, int
 // of each, and pairs of neighbouring tokens meet in one byte permutation (d_kv) or in the
 // rounding of two scaled codes to bf16 (e). A register set is requested again, for the step
 // after next, as soon as it is written to LDS, so that its loads have a whole step.
-template <bool F32, bool ADD>
+//
+// FINE: a step is 32 tokens, chunks 0 to 3 of d_kv's columns, and of e's the four chunks of the
+// first terms and the four of the second. A thread loads 4 columns of 8 tokens.
+template <bool F32, bool ADD, bool FINE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tiles_k,
                  int tiles, int per) {
@@ -116,29 +150,31 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
   int n0, k0;
   grad_tile((int)blockIdx.x - split * tiles, tiles_n, tiles_k, n0, k0);
   const int t_first = split * per, t_last = min(op.T, t_first + per);
-  const int steps = ((t_last - t_first + kStep - 1) / kStep + 1) & ~1;      // a step of zeros if odd
+  constexpr int kTokens = kStep<FINE>;
+  const int steps = ((t_last - t_first + kTokens - 1) / kTokens + 1) & ~1;  // a step of zeros if odd
   if (gridDim.x > (unsigned)tiles) grad = reinterpret_cast<float *>(grad) + (int64_t)split * op.N * op.K;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wk = wave >> 1, wn = wave & 1;
-  // a thread's 8 tokens (group) and 8 columns
-  const int tg = tid >> 5, tc = tid & 31;
-  const int d_v = tg * 8 * op.N * 2 + tc * 16, e_v = tg * 8 * op.K + tc * 8;
-  // f(c) = (c ^ c / 8) % 8: eight columns of a thread's, and eight threads' columns of the
-  // same number, lie in different slots
-  const int w_base = tc * 8 * kRow, w_x = tg ^ (tc & 7);
+  // a thread's 8 tokens (group) and 8 (FINE: 4) columns
+  constexpr int kCols = FINE ? 4 : 8;
+  const int tg = tid / (kTile / kCols), tc = tid % (kTile / kCols);
+  const int d_v = tg * 8 * op.N * 2 + tc * kCols * 2, e_v = tg * 8 * op.K + tc * kCols;
+  // f(c) = (c ^ c / 8) % 8: a thread's columns, and eight threads' columns of the same number,
+  // lie in different slots
+  const int w_base = tc * kCols * kRow, w_x = FINE ? tg ^ (tc & 1) * 4 ^ (tc >> 1 & 7) : tg ^ (tc & 7);
   const int frow = lane & 31, h = lane >> 5;
   const int a_base = (wk * 128 + frow) * kRow, b_base = (wn * 128 + frow) * kRow;
   const int f_x = (frow ^ frow >> 3) & 7;
 #define GR_D(st) ((st) ? d1 : d0)
 #define GR_E(st) ((st) ? e1 : e0)
-  uint4 dv[8];
-  uint2 ev[8];
+  std::conditional_t<FINE, uint2, uint4> dv[8];
+  std::conditional_t<FINE, uint32_t, uint2> ev[8];
   float4 sv[2];
 // Rows behind the last token are zeros.
 #define GR_ROWS(kt_)                                                                           \
-    const int t_ = t_first + (kt_) * kStep;                                                    \
-    const int rows_ = t_ >= t_last ? 0 : t_last - t_ < kStep ? t_last - t_ : kStep;            \
+    const int t_ = t_first + (kt_) * kTokens;                                                  \
+    const int rows_ = t_ >= t_last ? 0 : t_last - t_ < kTokens ? t_last - t_ : kTokens;        \
     const int64_t at_ = rows_ > 0 ? t_ : 0;
 // requests d_kv of step kt_, or its codes and scales
 #define GR_LOADD(kt_)                                                                          \
@@ -147,7 +183,10 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(                       \
         const_cast<uint16_t *>(op.d_kv + at_ * op.N + n0), 0,                                  \
         rows_ > 0 ? (rows_ * op.N - n0) * 2 : 0, kBufferFlags);                                \
-    _Pragma("unroll") for (int r = 0; r < 8; ++r) dv[r] = load16(rs, d_v, r * op.N * 2);       \
+    _Pragma("unroll") for (int r = 0; r < 8; ++r) {                                            \
+      if constexpr (FINE) dv[r] = load8(rs, d_v, r * op.N * 2);                                \
+      else dv[r] = load16(rs, d_v, r * op.N * 2);                                              \
+    }                                                                                          \
   }
 #define GR_LOADE(kt_)                                                                          \
   {                                                                                            \
@@ -158,35 +197,50 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
     const __amdgpu_buffer_rsrc_t rsS = __builtin_amdgcn_make_buffer_rsrc(                      \
         const_cast<float *>(op.e_scales + at_), 0, rows_ * 4, kBufferFlags);                   \
     _Pragma("unroll") for (int r = 0; r < 8; ++r) {                                            \
-      const auto v_ = __builtin_amdgcn_raw_buffer_load_b64(rs, e_v, r * op.K, 0);              \
-      ev[r] = make_uint2((uint32_t)v_[0], (uint32_t)v_[1]);                                    \
+      if constexpr (FINE) ev[r] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, e_v, r * op.K, 0); \
+      else ev[r] = load8(rs, e_v, r * op.K);                                                   \
     }                                                                                          \
     _Pragma("unroll") for (int r = 0; r < 2; ++r)                                              \
       sv[r] = __builtin_bit_cast(float4, load16(rsS, tg * 32, r * 16));                        \
   }
-#define GR_AT(buf, j) (*reinterpret_cast<uint4 *>(&(buf)[w_base + (j) * kRow + ((w_x ^ (j)) << 4)]))
+#define GR_AT(buf, j, x) (*reinterpret_cast<uint4 *>(&(buf)[w_base + (j) * kRow + ((w_x ^ (j) ^ (x)) << 4)]))
 // column j of d_kv: the low or high halves of word j / 2 of the 8 tokens, in pairs
-#define GR_WORD(v, at) ((at) == 0 ? (v).x : (at) == 1 ? (v).y : (at) == 2 ? (v).z : (v).w)
 #define GR_PAIR(r, j)                                                                          \
-  __builtin_amdgcn_perm(GR_WORD(dv[(r) + 1], (j) / 2), GR_WORD(dv[r], (j) / 2), (j) & 1 ? 0x07060302u : 0x05040100u)
+  __builtin_amdgcn_perm(word_of(dv[(r) + 1], (j) / 2), word_of(dv[r], (j) / 2), (j) & 1 ? 0x07060302u : 0x05040100u)
 #define GR_WRITED(st)                                                                          \
-  _Pragma("unroll") for (int j = 0; j < 8; ++j)                                                \
-    GR_AT(GR_D(st), j) = make_uint4(GR_PAIR(0, j), GR_PAIR(2, j), GR_PAIR(4, j), GR_PAIR(6, j));
-// columns 4 q .. 4 q + 3 of e
-#define GR_CODE(r, q, j) ((float)(int8_t)(((q) ? ev[r].y : ev[r].x) >> (8 * (j))))
+  _Pragma("unroll") for (int j = 0; j < kCols; ++j)                                            \
+    GR_AT(GR_D(st), j, 0) = make_uint4(GR_PAIR(0, j), GR_PAIR(2, j), GR_PAIR(4, j), GR_PAIR(6, j));
+// columns 4 q .. 4 q + 3 of e; FINE: both terms of columns 2 q and 2 q + 1
+#define GR_CODE(r, c) ((float)(int8_t)(word_of(ev[r], (c) / 4) >> (8 * ((c) & 3))))
+#define GR_VALUE(r, j) (GR_CODE(r, j) * ((r) % 4 == 0 ? sv[(r) / 4].x : (r) % 4 == 1 ? sv[(r) / 4].y : \
+                                         (r) % 4 == 2 ? sv[(r) / 4].z : sv[(r) / 4].w))
 #define GR_WRITEE(st, q)                                                                       \
-  _Pragma("unroll") for (int j = 0; j < 4; ++j)                                                \
-    GR_AT(GR_E(st), 4 * (q) + j) = make_uint4(                                                 \
-        engram::pack_bf16x2(GR_CODE(0, q, j) * sv[0].x, GR_CODE(1, q, j) * sv[0].y),           \
-        engram::pack_bf16x2(GR_CODE(2, q, j) * sv[0].z, GR_CODE(3, q, j) * sv[0].w),           \
-        engram::pack_bf16x2(GR_CODE(4, q, j) * sv[1].x, GR_CODE(5, q, j) * sv[1].y),           \
-        engram::pack_bf16x2(GR_CODE(6, q, j) * sv[1].z, GR_CODE(7, q, j) * sv[1].w));
-// fragments s of a step: half h of a wave takes tokens 8 (4 h + s) .. + 7
-#define GR_FRAG(buf, base, i, s)                                                               \
-  (*reinterpret_cast<const bf16x8 *>(&(buf)[(base) + (i) * 32 * kRow + (((4 * h + (s)) ^ f_x ^ ((i) * 4 & 7)) << 4)]))
+  if constexpr (FINE) {                                                                        \
+    _Pragma("unroll") for (int j = 2 * (q); j < 2 * (q) + 2; ++j) {                            \
+      uint4 high_, low_;                                                                       \
+      two_terms(GR_VALUE(0, j), GR_VALUE(1, j), high_.x, low_.x);                              \
+      two_terms(GR_VALUE(2, j), GR_VALUE(3, j), high_.y, low_.y);                              \
+      two_terms(GR_VALUE(4, j), GR_VALUE(5, j), high_.z, low_.z);                              \
+      two_terms(GR_VALUE(6, j), GR_VALUE(7, j), high_.w, low_.w);                              \
+      GR_AT(GR_E(st), j, 0) = high_;                                                           \
+      GR_AT(GR_E(st), j, 4) = low_;                                                            \
+    }                                                                                          \
+  } else {                                                                                     \
+    _Pragma("unroll") for (int j = 4 * (q); j < 4 * (q) + 4; ++j)                              \
+      GR_AT(GR_E(st), j, 0) = make_uint4(engram::pack_bf16x2(GR_VALUE(0, j), GR_VALUE(1, j)),  \
+                                         engram::pack_bf16x2(GR_VALUE(2, j), GR_VALUE(3, j)),  \
+                                         engram::pack_bf16x2(GR_VALUE(4, j), GR_VALUE(5, j)),  \
+                                         engram::pack_bf16x2(GR_VALUE(6, j), GR_VALUE(7, j))); \
+  }
+// fragments s of a step: half h of a wave takes tokens 8 (4 h + s) .. + 7; FINE: tokens 8 (2 (s / 2)
+// + h) .. + 7, of e the first terms where s is even, the second where it is odd
+#define GR_FRAG(buf, base, i, c)                                                               \
+  (*reinterpret_cast<const bf16x8 *>(&(buf)[(base) + (i) * 32 * kRow + (((c) ^ f_x ^ ((i) * 4 & 7)) << 4)]))
 #define GR_FRAGS(st, s, fa, fb)                                                                \
-  _Pragma("unroll") for (int i = 0; i < 4; ++i) fa[i] = GR_FRAG(GR_E(st), a_base, i, s);       \
-  _Pragma("unroll") for (int j = 0; j < 4; ++j) fb[j] = GR_FRAG(GR_D(st), b_base, j, s);
+  _Pragma("unroll") for (int i = 0; i < 4; ++i)                                                \
+    fa[i] = GR_FRAG(GR_E(st), a_base, i, FINE ? (s) % 2 * 4 + (s) / 2 * 2 + h : 4 * h + (s));  \
+  _Pragma("unroll") for (int j = 0; j < 4; ++j)                                                \
+    fb[j] = GR_FRAG(GR_D(st), b_base, j, FINE ? (s) / 2 * 2 + h : 4 * h + (s));
 #define GR_MFMA(fa, fb)                                                                        \
   _Pragma("unroll") for (int i = 0; i < 4; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j)  \
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
@@ -256,9 +310,9 @@ void grad_kernel(GradOperands op, void *__restrict__ grad, int tiles_n, int tile
 #undef GR_STEP
 #undef GR_MIX
 #undef GR_GROUP
+#undef GR_VALUE
 #undef GR_CODE
 #undef GR_PAIR
-#undef GR_WORD
 #undef GR_AT
 #undef GR_WRITEE
 #undef GR_WRITED
@@ -324,7 +378,7 @@ size_t engram_gemm_grad_workspace(int64_t t, int64_t n, int64_t k) {
 }
 
 hipError_t engram_launch_gemm_grad(const uint16_t *d_kv, const int8_t *e_codes, const float *e_scales,
-                                   bool f32, void *grad, int accumulate, int64_t t, int64_t n,
+                                   bool f32, bool fine, void *grad, int accumulate, int64_t t, int64_t n,
                                    int64_t k, float *workspace, hipStream_t stream) {
   const GradOperands op{d_kv, e_codes, e_scales, (int)t, (int)n, (int)k};
   const int tiles_n = (int)((n + kTile - 1) / kTile), tiles_k = (int)((k + kTile - 1) / kTile);
@@ -334,10 +388,15 @@ hipError_t engram_launch_gemm_grad(const uint16_t *d_kv, const int8_t *e_codes, 
   if (err != hipSuccess) return err;
   const int splits = workspace != nullptr ? grad_splits(t, n, k, cus) : 1;
   // whole steps a split
-  const int per = (int)(((t + splits - 1) / splits + kStep - 1) / kStep * kStep);
+  const int per = (int)(((t + splits - 1) / splits + 63) / 64 * 64);
   if (splits > 1) {
-    hipLaunchKernelGGL((grad_kernel<true, false>), dim3((unsigned)(tiles * splits)), dim3(256), 0, stream, op,
-                       workspace, tiles_n, tiles_k, tiles, per);
+    const dim3 blocks((unsigned)(tiles * splits));
+    if (fine)
+      hipLaunchKernelGGL((grad_kernel<true, false, true>), blocks, dim3(256), 0, stream, op, workspace, tiles_n,
+                         tiles_k, tiles, per);
+    else
+      hipLaunchKernelGGL((grad_kernel<true, false, false>), blocks, dim3(256), 0, stream, op, workspace, tiles_n,
+                         tiles_k, tiles, per);
     const int64_t quads = n * k / 4;
     const dim3 grid((unsigned)((quads + 255) / 256));
     if (f32)
@@ -347,13 +406,15 @@ hipError_t engram_launch_gemm_grad(const uint16_t *d_kv, const int8_t *e_codes, 
       hipLaunchKernelGGL((grad_join_kernel<false>), grid, dim3(256), 0, stream, workspace, splits, grad,
                          accumulate, quads);
   } else {
-#define ENGRAM_GRAD(F, A)                                                                       \
-  hipLaunchKernelGGL((grad_kernel<F, A>), dim3((unsigned)tiles), dim3(256), 0, stream, op, grad, \
+#define ENGRAM_GRAD(F, A, X)                                                                       \
+  hipLaunchKernelGGL((grad_kernel<F, A, X>), dim3((unsigned)tiles), dim3(256), 0, stream, op, grad, \
                      tiles_n, tiles_k, tiles, per)
-    if (f32 && accumulate) ENGRAM_GRAD(true, true);
-    else if (f32) ENGRAM_GRAD(true, false);
-    else if (accumulate) ENGRAM_GRAD(false, true);
-    else ENGRAM_GRAD(false, false);
+    if (fine && accumulate) ENGRAM_GRAD(true, true, true);
+    else if (fine) ENGRAM_GRAD(true, false, true);
+    else if (f32 && accumulate) ENGRAM_GRAD(true, true, false);
+    else if (f32) ENGRAM_GRAD(true, false, false);
+    else if (accumulate) ENGRAM_GRAD(false, true, false);
+    else ENGRAM_GRAD(false, false, false);
 #undef ENGRAM_GRAD
   }
   return hipGetLastError();

@@ -163,9 +163,10 @@ size_t engram_gate_grad_workspace(bool f32, int64_t tokens, int32_t hc, int32_t 
 hipError_t engram_launch_gate_grad(const EngramGateGrad &g, int64_t tokens, int32_t hc, int32_t dim,
                                    float eps, float clamp, int plain, hipStream_t stream);
 
-// The projection weight's gradient [n, k] from d_kv bf16 [t, n] and codes [t, k]. The
-// workspace, or NULL, holds engram_gemm_grad_workspace bytes.
+// The projection weight's gradient [n, k] from d_kv bf16 [t, n] and codes [t, k]; fine (with
+// f32): scaled codes in two bf16 terms. The workspace, or NULL, holds
+// engram_gemm_grad_workspace bytes.
 size_t engram_gemm_grad_workspace(int64_t t, int64_t n, int64_t k);
 hipError_t engram_launch_gemm_grad(const uint16_t *d_kv, const int8_t *e_codes, const float *e_scales,
-                                   bool f32, void *grad, int accumulate, int64_t t, int64_t n,
+                                   bool f32, bool fine, void *grad, int accumulate, int64_t t, int64_t n,
                                    int64_t k, float *workspace, hipStream_t stream);

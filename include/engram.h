@@ -191,8 +191,10 @@ typedef struct engram_short_conv {
 typedef enum engram_float_type {
   ENGRAM_BF16 = 0,
   ENGRAM_F32 = 1,
-  ENGRAM_I8 = 2               /* engram_gate_saved only: engram_quantize_i8's codes,
+  ENGRAM_I8 = 2,              /* engram_gate_saved only: engram_quantize_i8's codes,
                                  one fp32 scale per row                            */
+  ENGRAM_F32_FINE = 3         /* engram_project_grad only: fp32, from products in two
+                                 bf16 terms                                        */
 } engram_float_type;
 
 /* The scale that engram_quantize_i8 gives a row of largest magnitude amax. */
@@ -903,10 +905,14 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
  * Gradient of the projection's weight from its inputs in 8-bit codes (the operand of
  * engram_project_i8, or a checkpoint of e): grad[c, k] = sum_t d_kv[t, c] e_scales[t]
  * e[t, k], fp32 accumulation in the bf16 MFMA. e_scales[t] e[t, k] is rounded to bf16
- * first, which ENGRAM_SCALE_POW2 scales make exact.
+ * first, by up to 2^-8 of itself; ENGRAM_SCALE_POW2 scales make it exact. With others a
+ * gradient is off by about 1.7e-3 of its size in either type, for which
+ * ENGRAM_F32_FINE is there: e_scales[t] e[t, k] to within 2^-17 of itself, as the
+ * sum of two bf16 numbers, in about twice the time.
  *   d_kv      bf16 [tokens, out_dim], 16-byte aligned
  *   e_codes   int8 [tokens, in_dim], 16-byte aligned
  *   e_scales  float [tokens], 16-byte aligned
+ *   grad_type ENGRAM_BF16, ENGRAM_F32 or ENGRAM_F32_FINE (fp32 too)
  *   grad      grad_type [out_dim, in_dim], 16-byte aligned; accumulate 1: the sums are
  *             added to it, 0: it is overwritten (with zeros for no tokens)
  *   in_dim, out_dim, tokens  as engram_project_i8; out_dim <= ENGRAM_MAX_GRAD_OUT_DIM,

@@ -105,6 +105,19 @@ def test_products_refuse_types_pointers_and_workspaces():
     assert _weight_grad([P, P, P, None], tokens=0) == E.EINVAL
 
 
+def test_fine_gradients_are_the_weight_gradients_alone():
+    assert _weight_grad([None] * 4, tokens=0, accumulate=1, grad_type=E.F32_FINE) == E.OK
+    assert _weight_grad([P, P, P, None], tokens=0, grad_type=E.F32_FINE) == E.EINVAL
+    assert _weight_grad(grad_type=E.F32_FINE + 1) == E.EINVAL
+    assert _project(kv_type=E.F32_FINE) == E.EINVAL
+    assert _quantize(src_type=E.F32_FINE) == E.EINVAL
+    assert _gate(saved=_saved(kv_type=E.F32_FINE)) == E.EINVAL
+    assert _gate(saved=_saved(h_type=E.F32_FINE)) == E.EINVAL
+    for kw in (dict(table_type=E.F32_FINE), dict(out_type=E.F32_FINE)):
+        d = E.embed_desc(10, 4, 16, **kw)
+        assert _status("engram_embed", ctypes.byref(d), P, P, P, None) == E.EINVAL
+
+
 def _desc(**kw):
     base = dict(batch=1, seq=4, hc=4, dim=64, table_rows=0, row_format=E.ROW_E4M3_E8M0_264, row_dim=256)
     base.update(kw)

@@ -542,6 +542,129 @@ def test_weight_gradient_added_to_bf16():
     assert torch.equal(got, (plain + base.float()).to(torch.bfloat16))
 
 
+TYPES[E.F32_FINE] = torch.float32
+
+
+@pytest.mark.parametrize("grad_type", [E.BF16, E.F32, E.F32_FINE])
+@pytest.mark.parametrize("kind", [E.SCALE_F32, E.SCALE_POW2])
+@pytest.mark.parametrize("t,k,n", [(1, 48, 24), (65, 512, 256), (509, 176, 1032), (4096, 256, 512)])
+def test_weight_gradient_of_the_unrounded_values(t, k, n, kind, grad_type):
+    """Against e_scales e itself. Rounded to bf16, a value is off by at most 2^-8 of itself, and by
+    2^-24 in fp32 before; powers of two leave it as it is. The second of two terms is what the first
+    drops, at most 2^-8 of the value's power of two, so that a step of bf16 is at most 2^-16 there, and
+    a rounding 2^-17. What the sum adds is at most 2^-23 of the terms' magnitudes for each of them, which
+    are within 1 + 2^-7 of the unrounded values'."""
+    say("project_grad: unrounded values", t, k, n, kind, grad_type)
+    d_kv, codes, scales = weight_case(t, k, n, seed=t + k, kind=kind)
+    e, dt = scales.double()[:, None] * codes.double(), d_kv.double().t().contiguous()
+    want, mag = dt @ e, dt.abs() @ e.abs()
+    fine = grad_type == E.F32_FINE
+    part = 0.0 if kind == E.SCALE_POW2 else (2.0 ** -17 if fine else 2.0 ** -8) + 2.0 ** -23
+    err = ((t + 8) * (2 if fine else 1) * 2.0 ** -23 * (1 + 2.0 ** -7) + part) * mag
+    got = weight_grad(d_kv, codes, scales, grad_type)
+    off = (got.double() - want).abs()
+    tol = err + half_step(TYPES[grad_type]) * (want.abs() + err) + 1e-37
+    print("  off by %.2e of the norm" % float(off.norm() / want.norm()), flush=True)
+    assert (off <= tol).all(), (float((off - tol).max()), (off > tol).nonzero()[0].tolist())
+
+
+@pytest.mark.parametrize("t", [1, 7, 31, 32, 33, 64, 65, 96, 100, 128, 129, 160, 192, 224, 256, 300, 511, 1500])
+@pytest.mark.parametrize("k,n", [(16, 8), (48, 40), (304, 520)])
+def test_weight_gradient_in_two_terms(t, k, n):
+    """Whole numbers times 257 / 256 need 16 bits, which two terms hold and one does not. Their sums
+    stay below 2^24 (in units of 1 / 256: 1500 x 3 x 14 x 257), so that every order gives the same."""
+    say("project_grad: two terms", t, k, n)
+    g = torch.Generator(device=DEV).manual_seed(t)
+    d = torch.randint(-3, 4, (t, n), generator=g, device=DEV).to(torch.bfloat16)
+    codes = torch.randint(-14, 15, (t, k), generator=g, device=DEV, dtype=torch.int16).to(torch.int8)
+    scales = torch.full((t,), 257 / 256, device=DEV)
+    scales[::3] = 1.0
+    want = d.double().t().contiguous() @ (codes.double() * scales.double()[:, None])
+    base = torch.randint(-100, 100, (n, k), generator=g, device=DEV).float()
+    for workspace in (True, False):
+        got = weight_grad(d, codes, scales, E.F32_FINE, workspace=workspace)
+        assert torch.equal(got.double(), want)
+        got = weight_grad(d, codes, scales, E.F32_FINE, accumulate=1, grad=base, workspace=workspace)
+        assert torch.equal(got.double(), want + base.double())
+
+
+def test_weight_gradient_in_two_terms_of_every_code():
+    """The codes from -128 to 127 as whole columns, each against a single token's 1: what comes back is the
+    sum of a code's two terms."""
+    say("project_grad: two terms of every code")
+    codes = torch.arange(-128, 128, device=DEV, dtype=torch.int16).to(torch.int8).repeat(40, 1)
+    d = torch.eye(40, device=DEV).to(torch.bfloat16)
+    scales = torch.exp2(torch.randn(40, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV) * 20)
+    got = weight_grad(d, codes, scales, E.F32_FINE)
+    x = scales[:, None] * codes.float()
+    high = x.to(torch.bfloat16).float()
+    low = (x - high).to(torch.bfloat16).float()
+    assert torch.equal(got, high + low)
+    # powers of two are exact, as in one term
+    scales = (scales.view(torch.int32) & 0x7F800000).view(torch.float32)
+    assert torch.equal(weight_grad(d, codes, scales, E.F32_FINE), scales[:, None] * codes.float())
+
+
+def test_weight_gradient_in_two_terms_not_finite():
+    """What is infinite or NaN in one term is so in two: NaN and infinite scales, a product beyond
+    fp32's range, one that only its rounding to bf16 takes beyond, and d_kv's own."""
+    say("project_grad: two terms, not finite")
+    for scale, code in ((3.4e38, 127), (3.4e38 / 64, 64), (float("inf"), -3), (float("nan"), 5)):
+        d, c, s = weight_case(70, 160, 136, seed=5)
+        d[30], c[30], s[30] = 1.0, code, scale
+        got = weight_grad(d, c, s, E.F32_FINE)
+        assert (torch.isnan(got) if math.isnan(scale) else got == math.copysign(math.inf, code)).all()
+    d, c, s = weight_case(70, 160, 136, seed=5)
+    base = weight_grad(d, c, s, E.F32_FINE)
+    d[13, 9], d[20, 100] = float("nan"), float("inf")
+    got = weight_grad(d, c, s, E.F32_FINE)
+    keep = [i for i in range(136) if i not in (9, 100)]
+    assert torch.equal(got[keep], base[keep]) and torch.isnan(got[9]).all()
+    assert not torch.isfinite(got[100][c[20] != 0]).any()
+
+
+def test_weight_gradient_in_two_terms_of_no_tokens_far_offsets_and_replays():
+    say("project_grad: two terms, no tokens")
+    d, c, s = (torch.empty((0, n), dtype=x, device=DEV) for n, x in ((40, torch.bfloat16), (48, torch.int8),
+                                                                     (1, torch.float32)))
+    one = torch.ones((40, 48), device=DEV)
+    assert not weight_grad(d, c, s, E.F32_FINE, grad=one).any()
+    assert (weight_grad(d, c, s, E.F32_FINE, accumulate=1, grad=one) == 1).all()
+
+    say("project_grad: two terms, offsets beyond 2^31")
+    t, k, n = 88000, 64, 25600           # 2.25e9 values of d_kv
+    d = torch.zeros((t, n), dtype=torch.bfloat16, device=DEV)
+    c = torch.zeros((t, k), dtype=torch.int8, device=DEV)
+    s = torch.full((t,), 257 / 256, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    d[-3:] = torch.randint(-8, 9, (3, n), generator=g, device=DEV).to(torch.bfloat16)
+    c[-3:] = torch.randint(-128, 128, (3, k), generator=g, device=DEV, dtype=torch.int16).to(torch.int8)
+    got = weight_grad(d, c, s, E.F32_FINE)
+    assert torch.equal(got.double(), d[-3:].double().t().contiguous() @ c[-3:].double() * (257 / 256))
+    del d
+
+    say("project_grad: two terms, graphs")
+    cases = [weight_case(700, 272, 264, 1), weight_case(333, 1040, 1288, 2)]
+    bufs = []
+    for d, c, s in cases:
+        size = E.engram_project_grad_workspace_size(d.shape[0], c.shape[1], d.shape[1])
+        bufs.append((torch.empty((d.shape[1], c.shape[1]), device=DEV),
+                     torch.empty(max(size, 256), dtype=torch.uint8, device=DEV), size))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for x, b in zip(cases, bufs):
+            E.engram_project_grad(*x, b[0], E.F32_FINE, 0, x[0].shape[0], x[1].shape[1], x[0].shape[1], b[1], b[2])
+    for turn in range(4):
+        for x, b in zip(cases, bufs):
+            x[0].copy_(torch.randn_like(x[0].float()))
+            b[0].fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [b[0].clone() for b in bufs]
+        for x, y in zip(cases, got):
+            assert torch.equal(weight_grad(*x, E.F32_FINE), y)
+
+
 @pytest.mark.parametrize("t", [300, 1500])
 def test_weight_gradient_added_across_splits(t):
     """Few tiles and many tokens: with a workspace the tokens are split and joined. Whole
