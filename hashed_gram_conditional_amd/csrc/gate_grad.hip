@@ -14,9 +14,11 @@
 // products of h and k, and w = q_w k_w enters it as the product and its rounding error, so
 // that s keeps its relative precision there. Everything else is fp32.
 //
-// Bound by HBM: every byte is read or written once. A block walks the tokens blockIdx.x,
-// blockIdx.x + gridDim.x, ...; a thread owns 8 columns of every stream and keeps its part of
-// dw in registers over all of them. The blocks' parts are summed by a second launch in a
+// Bound by HBM: what the outputs need is read once and they are written once. (Beside that,
+// gate_grad_token_kernel requests a DEAD position's saved rows and reads its d_out again where
+// d_h is another buffer, and with a team's last token one more, which nothing uses.) A block walks
+// the tokens blockIdx.x, blockIdx.x + gridDim.x, ...; a thread owns 8 columns of every stream and
+// keeps its part of dw in registers over all of them. The blocks' parts are summed by a second launch in a
 // fixed order. 32768 tokens of 4 x 5120 from codes take 1.15 ms (5.88 GB, 5.1 TB/s; stream by
 // stream, with a barrier and a wait for loads at each, 2.89 ms; without the sums over the wave
 // 1.09 ms), 509 tokens 45 us, of which the stores take 10 and the second launch 5.
@@ -179,7 +181,11 @@ __device__ __forceinline__ void store_dead(const GateGradArgs &a, int64_t t, int
 // used up, so that a token is in flight while another is worked on. The learned scales lie
 // in LDS as w = q_w k_w rounded to fp32 and the part of it that this drops, 2^24 times that in
 // fp16: 36 bits in all (bf16 left dq_w of 32768 x 4 x 5120 off by 1.3e-6 of its norm where one
-// token's s came near 0, against 2e-7). A block has
+// token's s came near 0, against 2e-7). Registers spill inside the loop where they hold most: 13 with
+// 4 streams all in bf16, 10 with 4 all in fp32, with 8 streams 1 from codes, 34 and 56 from codes and
+// bf16, 84 from bf16; a reload waits for the loads requested before it. From bf16 arrays 8192 x 4 x
+// 5120 take 382 us (4.8 TB/s; from codes 311) and 4096 x 8 x 1024 175 us (2.0 TB/s; from codes 95).
+// A block has
 // `teams` teams of `width` threads, each on a token of its own, which share w; their parts
 // of dw meet in LDS at the end. F32: fp32 streams, else bf16. KI8, HI8: keys and value,
 // streams as codes.

@@ -12,11 +12,12 @@
 // them on the way through registers, where the codes have to pass anyway. Other ways measured
 // at 32768 x 25600 x 6144: LDS reads that transpose (ds_read_b64_tr_b16; half the rate of
 // 16-byte reads, 2650 cycles of LDS a step beside 2048 of the MFMAs) 10.0 ms; the codes scaled
-// and turned by a launch before, direct loads of them here, 10.0 ms; this 9.1-9.4 ms, 1.10-1.13
-// PFLOP/s. It is bound by power: 1.7-1.8 GHz, the matrix units 59 % busy; with codes and
-// gradients of zero the same kernel takes 7.5 ms, and MFMAs with LDS reads alone 6.3 ms.
-// 509 tokens take 223 us into fp32 (629 MB of gradients), of which each of the ten rounds of
-// tiles spends 13 us in its eight steps and 10 us in its first loads and its stores; one block
+// and turned by a launch before, direct loads of them here, 10.0 ms; this 9.1-9.5 ms, 1.09-1.13
+// PFLOP/s. Power and stalls bound it together: the clock falls to 1.7-1.8 GHz, and the matrix units
+// are busy 59 % of that; with codes and gradients of zero the same kernel takes 7.5 ms, and MFMAs
+// with LDS reads alone 6.3 ms. 509 tokens take 223-230 us into fp32 (629 MB of gradients; 240 to 280
+// in the first hundred passes after idling), of which each of the ten rounds of tiles spends 13 us
+// in its eight steps and 10 us in its first loads and its stores; one block
 // per CU that walks the tiles with the next one's loads ahead saved 2 % there and lost 9 %
 // in the long sum, whose addresses it had to form anew in every step.
 #include <type_traits>
@@ -94,8 +95,10 @@ __device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, 
 // Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 2 tiles of d_kv's
 // columns by all of e's, so that its 32 blocks share 2 panels of d_kv and 16 of codes. By the
 // bytes alone 4 by 8 would be less to read (512 bytes of d_kv a token and 256 of codes), but
-// measured 2 is ahead: 32768 x 25600 x 6144 in 9.18 ms, and 9.19, 9.33 and 9.8 in groups of
-// 1, 4 and 8.
+// measured 2 is ahead or within 1 % (tokens x d_kv's columns x e's, us in groups of 1, 2, 4 and 8):
+// 32768 x 25600 x 6144 9190, 9130, 9290, 9580; 32768 x 5120 x 6144 1771, 1755, 1760, 1796; 8192 x
+// 8192 x 8192 926, 912, 915, 922; 16384 x 25600 x 1024 815, 825, 832, 841; 16384 x 1536 x 6144 386,
+// 384, 388, 390; 16384 x 1024 x 25600 830, 822, 827, 827.
 constexpr int kGroupN = 2;
 
 // Two scaled values, as pairs of bf16 numbers: their roundings, and the roundings of what those
@@ -357,7 +360,12 @@ __global__ __launch_bounds__(256) void grad_join_kernel(const float *__restrict_
 }
 
 // How many parts the tokens are split into: as many as fit the CUs beside each other, each
-// of at least 256 tokens.
+// of at least 256 tokens, so that only up to half as many tiles as CUs are split. Split and
+// whole (us, fp32, tokens x e's columns x d_kv's, parts): 512 x 1024 x 1024, 2: 20, 20; 600 x 512 x
+// 512, 3: 18, 22; 1024 x 1024 x 1024, 4: 22, 30; 4096 x 1024 x 1024, 16: 37, 91; 4096 x 2048 x 4096,
+// 2: 91, 100; 8192 x 6144 x 1024, 2: 123, 175; 32768 x 1536 x 2560, 4: 266, 748. Above half, tiles
+// of 129 to 255, whole: 4096 x 6144 x 1536 (144 tiles) 95, 32768 x 6144 x 1536 750, 32768 x 4096 x
+// 2560 (160) 756, with the other CUs idle.
 int grad_splits(int64_t t, int64_t n, int64_t k, int cus) {
   const int64_t tiles = ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
   const int64_t most = (t + 255) / 256, fit = cus / tiles;

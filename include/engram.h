@@ -849,8 +849,8 @@ int engram_quantize_i8(const void *src, int32_t src_type, int64_t rows, int64_t 
  *   kv        kv_type [tokens, out_dim], 16-byte aligned
  *   in_dim    a multiple of 16, at most ENGRAM_MAX_I8_IN_DIM; out_dim % 8 == 0; the
  *             tile bound of engram_project
- *   workspace as for engram_project, sized by engram_project_i8_workspace_size. The
- *             result does not depend on it
+ *   workspace NULL, or 256-byte aligned; not used so far, and
+ *             engram_project_i8_workspace_size is 0 for every call
  * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
  */
 int engram_project_i8(const void *e_codes, const float *e_scales, const void *w_codes,
@@ -858,8 +858,8 @@ int engram_project_i8(const void *e_codes, const float *e_scales, const void *w_
                       int64_t in_dim, int64_t out_dim, void *workspace, size_t workspace_bytes,
                       hipStream_t stream);
 
-/* [host] Bytes of workspace engram_project_i8 uses on the current device (0: none, bad
- * arguments or a HIP error). */
+/* [host] Bytes of workspace engram_project_i8 uses on the current device: 0 for every
+ * call so far, none being needed. */
 size_t engram_project_i8_workspace_size(int64_t tokens, int64_t in_dim, int64_t out_dim);
 
 /*
@@ -909,7 +909,8 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
  * gradient is off by about 1.7e-3 of its size in either type, for which
  * ENGRAM_F32_FINE is there: e_scales[t] e[t, k] to within 2^-17 of itself, as the
  * sum of two bf16 numbers, in about twice the time.
- *   d_kv      bf16 [tokens, out_dim], 16-byte aligned
+ *   d_kv      bf16 [tokens, out_dim], 16-byte aligned. An ENGRAM_ROW_F32 layer's, which
+ *             engram_gate_grad writes in fp32, is rounded to bf16 by the caller first
  *   e_codes   int8 [tokens, in_dim], 16-byte aligned
  *   e_scales  float [tokens], 16-byte aligned
  *   grad_type ENGRAM_BF16, ENGRAM_F32 or ENGRAM_F32_FINE (fp32 too)
@@ -918,8 +919,9 @@ int engram_gate_grad(const engram_forward_desc *desc, const int32_t *ids, int32_
  *   in_dim, out_dim, tokens  as engram_project_i8; out_dim <= ENGRAM_MAX_GRAD_OUT_DIM,
  *             tokens <= ENGRAM_MAX_GRAD_TOKENS
  *   workspace NULL, or at least engram_project_grad_workspace_size bytes, 256-byte
- *             aligned: calls with fewer output tiles than the GPU has CUs then split
- *             the tokens over them, with fp32 parts summed in a fixed order
+ *             aligned: calls of more than 256 tokens with at most half as many output
+ *             tiles (256 x 256) as the GPU has CUs then split the tokens over them, with
+ *             fp32 parts summed in a fixed order
  * Errors: ENGRAM_EINVAL, ENGRAM_ESHAPE, ENGRAM_EWORKSPACE, ENGRAM_EHIP.
  */
 int engram_project_grad(const void *d_kv, const void *e_codes, const float *e_scales, void *grad,
