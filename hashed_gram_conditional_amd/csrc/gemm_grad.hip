@@ -92,15 +92,6 @@ __device__ __forceinline__ void store_patch(const f32x16 &a0, const f32x16 &a1, 
   }
 }
 
-// Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 2 tiles of d_kv's
-// columns by all of e's, so that its 32 blocks share 2 panels of d_kv and 16 of codes. By the
-// bytes alone 4 by 8 would be less to read (512 bytes of d_kv a token and 256 of codes), but
-// measured 2 is ahead or within 1 % (tokens x d_kv's columns x e's, us in groups of 1, 2, 4 and 8):
-// 32768 x 25600 x 6144 9190, 9130, 9290, 9580; 32768 x 5120 x 6144 1771, 1755, 1760, 1796; 8192 x
-// 8192 x 8192 926, 912, 915, 922; 16384 x 25600 x 1024 815, 825, 832, 841; 16384 x 1536 x 6144 386,
-// 384, 388, 390; 16384 x 1024 x 25600 830, 822, 827, 827.
-constexpr int kGroupN = 2;
-
 // Two scaled values, as pairs of bf16 numbers: their roundings, and the roundings of what those
 // drop, in all within 2^-17 of the value. A rounding that is not finite has nothing beside it.
 __device__ __forceinline__ void two_terms(float a, float b, uint32_t &high, uint32_t &low) {
@@ -121,6 +112,15 @@ __device__ __forceinline__ uint2 load8(__amdgpu_buffer_rsrc_t rs, int voff, int 
   const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0);
   return make_uint2((uint32_t)v[0], (uint32_t)v[1]);
 }
+
+// Tile `bid`: each XCD takes a contiguous range of tiles, in groups of 2 tiles of d_kv's
+// columns by all of e's, so that its 32 blocks share 2 panels of d_kv and 16 of codes. By the
+// bytes alone 4 by 8 would be less to read (512 bytes of d_kv a token and 256 of codes), but
+// measured 2 is ahead or within 1 % (tokens x d_kv's columns x e's, us in groups of 1, 2, 4 and 8):
+// 32768 x 25600 x 6144 9190, 9130, 9290, 9580; 32768 x 5120 x 6144 1771, 1755, 1760, 1796; 8192 x
+// 8192 x 8192 926, 912, 915, 922; 16384 x 25600 x 1024 815, 825, 832, 841; 16384 x 1536 x 6144 386,
+// 384, 388, 390; 16384 x 1024 x 25600 830, 822, 827, 827.
+constexpr int kGroupN = 2;
 
 __device__ __forceinline__ void grad_tile(int bid, int tiles_n, int tiles_k, int &n0, int &k0) {
   const int full = tiles_n * tiles_k / kXcds * kXcds;
